@@ -17,6 +17,10 @@
  *   cg_sample_advance_fill  the same, then the next step's bitmask (device)
  *   cg_sample_advance_plan, cg_fill_walk  its two launches, one call each
  *   cg_fill_draft        masks along each row's k-token draft (device)
+ *   cg_filter_sample     masked draw with top-k, top-p, min-p from given numbers (device)
+ *   cg_top_logits        the k largest masked logits and the normaliser (device)
+ *   cg_distill_topk      loss against a teacher's top logits, with its gradient (device)
+ *   cg_distill_topk_grad  the gradient alone, from the saved normaliser (device)
  *   cg_force_bytes       engine-written bytes (an evaluated result) (device)
  *   cg_eval_calc         evaluate a calc span (host)
  *   cg_eval_strop        evaluate a string-operation span (host)
@@ -352,6 +356,102 @@ int cg_sample_advance_plan(const cg_grammar *g, const void *d_logits, int32_t dt
                            void *stream);
 int cg_fill_walk(const cg_grammar *g, const cg_state *d_states, int32_t batch, uint64_t *d_mask,
                  int32_t words_per_row, void *d_workspace, void *stream);
+
+/* Largest vocabulary of the row operators below, and longest list of top logits. */
+#define CG_MAX_ROW_VOCAB 4194304
+#define CG_MAX_TOP 1024
+
+/* Bytes of the workspace cg_filter_sample needs for (batch, vocab) (0 if batch or vocab < 1). */
+size_t cg_filter_workspace_bytes(int32_t batch, int32_t vocab);
+
+/*
+ * A draw from the filtered distribution of each row, from a given uniform
+ * number ("Constrained decoding", "The guarantee": sampling runs after
+ * masking, so no sampling strategy can escape it).  Logits, dtype, stride
+ * and mask as for cg_apply_mask_sample; d_mask may be NULL (every id
+ * allowed).  Row r's candidates are the allowed ids whose logit is neither
+ * -inf nor NaN (masked logits may hold anything), ordered by falling logit,
+ * equal logits (the two zeros are equal) by rising id.  With T =
+ * d_temperature[r] > 0 and m the largest candidate logit, a candidate's
+ * weight is w = exp((x - m) / T) (1 where x = m, so a logit of +inf takes
+ * all), computed in 64 bits and held in units of 2^-40.  In this order:
+ *   top-k   ranks below k = d_top_k[r] stay (k <= 0: all);
+ *   top-p   rank j > 0 stays while the weight before it is less than
+ *           d_top_p[r] times the weight top-k left (>= 1 or NaN: all,
+ *           <= 0: rank 0 alone);
+ *   min-p   weights of at least d_min_p[r] stay (<= 0 or NaN: all, > 1: as 1).
+ * d_top_k, d_top_p, d_min_p may each be NULL: no such filter.  Rank 0 always
+ * stays.  The pick is the first kept rank up to which the weights sum to
+ * more than u S, S their whole sum and u = d_uniform[r] in [0, 1) (below 0
+ * or NaN: as 0; 1 and above: the last kept candidate that has weight);
+ * logprob = (x - m) / T - ln S.
+ *   T <= 0 or NaN: greedy, rank 0, whatever the filters; logprob as
+ *   cg_apply_mask_sample's for T = 0.
+ * No candidate: id = -1, logprob = 0.
+ * vocab <= CG_MAX_ROW_VOCAB.  d_workspace: cg_filter_workspace_bytes(batch,
+ * vocab) bytes, 16-byte aligned; may be NULL when that size is 0 (every
+ * intermediate is kept on chip, so it always is).
+ * Outputs: d_out_ids[batch] int32 (as cg_advance takes them),
+ * d_out_logprob[batch] float32.
+ */
+int cg_filter_sample(const void *d_logits, int32_t dtype, int32_t batch, int32_t vocab, int64_t row_stride,
+                     const uint64_t *d_mask, int32_t words_per_row, const float *d_temperature,
+                     const int32_t *d_top_k, const float *d_top_p, const float *d_min_p, const float *d_uniform,
+                     void *d_workspace, int32_t *d_out_ids, float *d_out_logprob, void *stream);
+
+/* Bytes of the workspace cg_top_logits needs (0 if an argument is < 1). */
+size_t cg_top_workspace_bytes(int32_t batch, int32_t vocab, int32_t k);
+
+/*
+ * The first k ranks of each row's candidates (the order of
+ * cg_filter_sample): d_out_ids[r * k + j] int32 and d_out_logits[r * k + j]
+ * float32 (the logit as it is), -1 and -inf past the last candidate, and
+ * d_out_lse[r] = ln sum exp(x) over all candidates (-inf without one), so
+ * that logit - lse is a token's log-probability under the mask: the record a
+ * student is trained on (cg_distill_topk) and the top log-probabilities of a
+ * reply.  1 <= k <= CG_MAX_TOP.  d_workspace: cg_top_workspace_bytes(batch,
+ * vocab, k) bytes, 16-byte aligned; may be NULL when that size is 0.
+ */
+int cg_top_logits(const void *d_logits, int32_t dtype, int32_t batch, int32_t vocab, int64_t row_stride,
+                  const uint64_t *d_mask, int32_t words_per_row, int32_t k, void *d_workspace, int32_t *d_out_ids,
+                  float *d_out_logits, float *d_out_lse, void *stream);
+
+/*
+ * Distillation from a teacher's top logits: row r holds the student's logits
+ * x (d_logits as above) at one position and the teacher's record there, ids
+ * d_teacher_ids[r * k + j] with logits t = d_teacher_logits[r * k + j].  The
+ * student's distribution is the masked one it decodes with, q_v = exp(x_v /
+ * tau - L), L = ln sum exp(x / tau) over its allowed logits above -inf; the
+ * teacher's is the softmax p of t / tau over the entries the student can
+ * take: 0 <= id < vocab, allowed, student logit above -inf, t above -inf
+ * (so -1 pads a shorter record).  An id may stand more than once; its
+ * entries add up.
+ *   loss = tau^2 sum_j p_j (ln p_j - ln q_{id_j});
+ *   d loss / d x_v = tau (q_v - sum of p_j with id_j = v) where v is
+ *   allowed, exactly 0 elsewhere.
+ * A row without an entry (a padded position, an empty mask) has loss 0 and
+ * gradient 0.  An allowed NaN makes the row's loss, normaliser and gradient
+ * NaN; masked logits may hold anything.
+ *   d_out_loss[rows]; d_out_lse[rows] = L (may be NULL; -inf for an empty
+ *   row), float32;
+ *   d_out_grad: NULL, or rows grad_stride elements apart in the logits'
+ *   dtype, receiving d_weight[r] times the row's gradient (d_weight[rows]:
+ *   the derivative of the caller's objective by each row's loss), elements
+ *   past vocab left untouched.  It may be d_logits itself with the same
+ *   stride; otherwise they must not overlap.
+ * temperature = tau, positive and finite; 1 <= k <= CG_MAX_TOP.
+ */
+int cg_distill_topk(const void *d_logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
+                    const uint64_t *d_mask, int32_t words_per_row, const int32_t *d_teacher_ids,
+                    const float *d_teacher_logits, int32_t k, float temperature, float *d_out_loss, float *d_out_lse,
+                    const float *d_weight, void *d_out_grad, int64_t grad_stride, void *stream);
+
+/* The gradient of cg_distill_topk alone: d_lse[rows] is that call's
+ * d_out_lse for the same logits, mask and temperature. */
+int cg_distill_topk_grad(const void *d_logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
+                         const uint64_t *d_mask, int32_t words_per_row, const int32_t *d_teacher_ids,
+                         const float *d_teacher_logits, int32_t k, float temperature, const float *d_lse,
+                         const float *d_weight, void *d_out_grad, int64_t grad_stride, void *stream);
 
 /*
  * Walk d_token_ids[r] for every row: -1 is a no-op (CG_ROW_NOOP).  A token

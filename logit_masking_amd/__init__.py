@@ -19,6 +19,7 @@ FLAG_DONE, FLAG_CAPPED = 1, 2
 HOST_ONLY = 1
 STATE_BYTES = 24
 DTYPE_F32, DTYPE_BF16 = 0, 1
+MAX_ROW_VOCAB, MAX_TOP = 4194304, 1024  # CG_MAX_ROW_VOCAB, CG_MAX_TOP
 FILL_NOALLOC_SCRATCH_BYTES = 16 << 20  # CG_FILL_NOALLOC_SCRATCH_BYTES
 
 # Symbols the C ABI (include/cg.h) exports.
@@ -27,7 +28,9 @@ EXPORTS = ["cg_compile_grammar", "cg_free_grammar", "cg_grammar_info", "cg_init_
            "cg_sample_advance_plan", "cg_fill_walk", "cg_force_bytes", "cg_eval_calc", "cg_draft_workspace_bytes",
            "cg_fill_draft", "cg_contract_model_spec", "cg_contract_reverse", "cg_cache_stats", "cg_cache_clear",
            "cg_eval_strop", "cg_fill_bitmask_noalloc",
-           "cg_sample_workspace_bytes", "cg_apply_mask_sample", "cg_advance", "cg_try_input", "cg_last_error"]
+           "cg_sample_workspace_bytes", "cg_apply_mask_sample", "cg_advance", "cg_try_input", "cg_last_error",
+           "cg_filter_workspace_bytes", "cg_filter_sample", "cg_top_workspace_bytes", "cg_top_logits",
+           "cg_distill_topk", "cg_distill_topk_grad"]
 
 
 class CgError(RuntimeError):
@@ -480,3 +483,273 @@ def apply_mask_sample(logits, mask, temperature, seed, step, workspace, out_ids,
     _check(lib().cg_apply_mask_sample(_ptr(logits), dt, B, V, logits.stride(0), _ptr(mask), mask.shape[1],
                                       _ptr(temperature), _ptr(seed), _ptr(step), _ptr(workspace), _ptr(out_ids),
                                       _ptr(out_logprob), _stream(stream)))
+
+
+# ---- row operators: filtered sampling, top logits, distillation ---------------
+# Every tensor of a call lives on the logits' device; the call runs on that
+# device's current stream (or `stream`), whatever device is current.
+
+_row_fns = None
+
+
+def _row_lib():
+    """The row operators' functions with their prototypes, set once."""
+    global _row_fns
+    if _row_fns is None:
+        L = lib()
+        vp, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+        rows = [vp, i32, i32, i32, i64, vp, i32]
+        for name, args, res in (
+                ("cg_filter_workspace_bytes", [i32, i32], sz),
+                ("cg_filter_sample", rows + [vp] * 9, ctypes.c_int),
+                ("cg_top_workspace_bytes", [i32, i32, i32], sz),
+                ("cg_top_logits", rows + [i32] + [vp] * 5, ctypes.c_int),
+                ("cg_distill_topk", rows + [vp, vp, i32, f32, vp, vp, vp, vp, i64, vp], ctypes.c_int),
+                ("cg_distill_topk_grad", rows + [vp, vp, i32, f32, vp, vp, vp, i64, vp], ctypes.c_int)):
+            fn = getattr(L, name)
+            fn.argtypes, fn.restype = args, res
+        _row_fns = L
+    return _row_fns
+
+
+def _rows(logits, mask, vocab):
+    """(dtype code, rows, vocab, row stride, mask address, words) of the logits and mask of a row operator."""
+    import torch
+    if logits.dtype is torch.bfloat16:
+        dt = DTYPE_BF16
+    elif logits.dtype is torch.float32:
+        dt = DTYPE_F32
+    else:
+        raise ValueError("logits must be float32 or bfloat16")
+    if logits.device.type != "cuda" or logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be a 2-D device tensor with unit column stride")
+    B, cols = logits.shape
+    V = cols if vocab is None else vocab
+    if not 1 <= V <= cols:
+        raise ValueError("vocab out of range of the logits' columns")
+    if V > MAX_ROW_VOCAB:
+        raise ValueError(f"vocab above {MAX_ROW_VOCAB}")
+    # a row of its own may have any stride
+    stride = max(logits.stride(0), V) if B == 1 else logits.stride(0)
+    if stride < V:
+        raise ValueError("logits' rows overlap")
+    if mask is None:
+        return dt, B, V, stride, None, 0
+    _row_arg(mask, torch.int64, "mask", logits, (B, None))
+    if mask.shape[1] < (V + 63) // 64:
+        raise ValueError("mask has fewer than ceil(vocab / 64) words per row")
+    return dt, B, V, stride, mask.data_ptr(), mask.shape[1]
+
+
+def _row_arg(t, dtype, name, logits, shape):
+    """A contiguous tensor beside the logits with at least shape[0] rows (and exactly shape[1] columns); its address."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != logits.device:
+        raise ValueError(f"{name} must be on the logits' device")
+    if t.dim() != len(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {len(shape)} dims")
+    if t.shape[0] < shape[0]:
+        raise ValueError(f"{name} has fewer rows than logits")
+    if len(shape) > 1 and shape[1] is not None and t.shape[1] != shape[1]:
+        raise ValueError(f"{name} must have {shape[1]} columns")
+    return t.data_ptr()
+
+
+def _workspace_arg(t, need, logits):
+    if t is None:
+        if need:
+            raise ValueError("a workspace is needed")
+        return None
+    if t.device != logits.device or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous on the logits' device")
+    if t.numel() * t.element_size() < need:
+        raise ValueError("workspace too small")
+    return t.data_ptr()
+
+
+def _row_call(fn, logits, stream, *args):
+    """fn(*args, stream) on the logits' device."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(logits.device)
+    raw = getattr(stream, "cuda_stream", stream) or 0
+    if logits.device.index != torch.cuda.current_device():
+        with torch.cuda.device(logits.device):
+            rc = fn(*args, raw)
+    else:
+        rc = fn(*args, raw)
+    if rc != CG_OK:
+        _check(rc)
+
+
+def filter_workspace_bytes(B: int, V: int) -> int:
+    return int(_row_lib().cg_filter_workspace_bytes(B, V))
+
+
+def new_filter_workspace(B: int, V: int, device="cuda"):
+    """A workspace for filter_sample (possibly empty)."""
+    import torch
+    return torch.empty((filter_workspace_bytes(B, V) + 15) // 16 * 2, dtype=torch.int64, device=device)
+
+
+def filter_sample(logits, mask, temperature, top_k, top_p, min_p, uniform, workspace, out_ids, out_logprob, vocab=None,
+                  stream=None):
+    """cg_filter_sample on torch tensors: logits [B, >= vocab] float32 or
+    bfloat16, mask [B, W] int64 or None, temperature [B] float32, top_k [B]
+    int32, top_p and min_p [B] float32 (each of the three may be None: no such
+    filter), uniform [B] float32 in [0, 1); workspace from
+    new_filter_workspace(B, vocab) or None; outputs ids [B] int32, logprob [B]
+    float32."""
+    import torch
+    L = _row_lib()
+    dt, B, V, stride, m, words = _rows(logits, mask, vocab)
+    f32, i32, n = torch.float32, torch.int32, (B,)
+    _row_call(L.cg_filter_sample, logits, stream, logits.data_ptr(), dt, B, V, stride, m, words,
+              _row_arg(temperature, f32, "temperature", logits, n),
+              None if top_k is None else _row_arg(top_k, i32, "top_k", logits, n),
+              None if top_p is None else _row_arg(top_p, f32, "top_p", logits, n),
+              None if min_p is None else _row_arg(min_p, f32, "min_p", logits, n),
+              _row_arg(uniform, f32, "uniform", logits, n),
+              _workspace_arg(workspace, L.cg_filter_workspace_bytes(B, V), logits),
+              _row_arg(out_ids, i32, "out_ids", logits, n), _row_arg(out_logprob, f32, "out_logprob", logits, n))
+
+
+def top_workspace_bytes(B: int, V: int, k: int) -> int:
+    return int(_row_lib().cg_top_workspace_bytes(B, V, k))
+
+
+def new_top_workspace(B: int, V: int, k: int, device="cuda"):
+    """A workspace for top_logits (possibly empty)."""
+    import torch
+    return torch.empty((top_workspace_bytes(B, V, k) + 15) // 16 * 2, dtype=torch.int64, device=device)
+
+
+def top_logits(logits, mask, workspace, out_ids, out_logits, out_lse, vocab=None, stream=None):
+    """cg_top_logits on torch tensors: logits and mask as for filter_sample,
+    workspace from new_top_workspace(B, vocab, k) or None; outputs ids [B, k]
+    int32, logits [B, k] float32 (k <= MAX_TOP is their column count), lse [B]
+    float32."""
+    import torch
+    L = _row_lib()
+    dt, B, V, stride, m, words = _rows(logits, mask, vocab)
+    if out_ids.dim() != 2:
+        raise ValueError("out_ids must be [B, k]")
+    k = out_ids.shape[1]
+    _row_call(L.cg_top_logits, logits, stream, logits.data_ptr(), dt, B, V, stride, m, words, k,
+              _workspace_arg(workspace, L.cg_top_workspace_bytes(B, V, k), logits),
+              _row_arg(out_ids, torch.int32, "out_ids", logits, (B, k)),
+              _row_arg(out_logits, torch.float32, "out_logits", logits, (B, k)),
+              _row_arg(out_lse, torch.float32, "out_lse", logits, (B,)))
+
+
+def _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab):
+    import torch
+    dt, B, V, stride, m, words = _rows(logits, mask, vocab)
+    if teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids must be [rows, k]")
+    k = teacher_ids.shape[1]
+    return B, V, (logits.data_ptr(), dt, B, V, stride, m, words,
+                  _row_arg(teacher_ids, torch.int32, "teacher_ids", logits, (B, k)),
+                  _row_arg(teacher_logits, torch.float32, "teacher_logits", logits, (B, k)), k, temperature)
+
+
+def _grad_arg(grad, logits, B, V):
+    """(address, row stride) of a gradient: the logits themselves, or rows apart from them."""
+    if grad.dtype is not logits.dtype or grad.device != logits.device:
+        raise ValueError("out_grad must have the logits' dtype and device")
+    if grad.dim() != 2 or grad.stride(1) != 1 or grad.shape[0] < B or grad.shape[1] < V:
+        raise ValueError("out_grad must be [rows, >= vocab] with unit column stride")
+    stride = max(grad.stride(0), V) if B == 1 else grad.stride(0)
+    if stride < V:
+        raise ValueError("out_grad's rows overlap")
+    a, b = grad.data_ptr(), logits.data_ptr()
+    if a != b or stride != (max(logits.stride(0), V) if B == 1 else logits.stride(0)):
+        size = logits.element_size()
+        if B and a < b + ((B - 1) * logits.stride(0) + V) * size and b < a + ((B - 1) * stride + V) * size:
+            raise ValueError("out_grad overlaps the logits (it may only be the same rows)")
+    return a, stride
+
+
+def distill_topk(logits, mask, teacher_ids, teacher_logits, temperature, out_loss, out_lse=None, weight=None,
+                 out_grad=None, vocab=None, stream=None):
+    """cg_distill_topk on torch tensors: student logits [rows, >= vocab]
+    float32 or bfloat16, mask [rows, W] int64 or None, teacher_ids [rows, k]
+    int32, teacher_logits [rows, k] float32 (what top_logits writes),
+    temperature a number; outputs loss [rows] float32, lse [rows] float32 or
+    None and, given weight [rows] float32, the gradient of sum(weight * loss)
+    in out_grad [rows, >= vocab] of the logits' dtype (it may be `logits`)."""
+    import torch
+    L = _row_lib()
+    B, V, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
+    f32 = torch.float32
+    if (weight is None) != (out_grad is None):
+        raise ValueError("weight and out_grad go together")
+    g, gs = (None, 0) if out_grad is None else _grad_arg(out_grad, logits, B, V)
+    _row_call(L.cg_distill_topk, logits, stream, *args, _row_arg(out_loss, f32, "out_loss", logits, (B,)),
+              None if out_lse is None else _row_arg(out_lse, f32, "out_lse", logits, (B,)),
+              None if weight is None else _row_arg(weight, f32, "weight", logits, (B,)), g, gs)
+
+
+def distill_topk_grad(logits, mask, teacher_ids, teacher_logits, temperature, lse, weight, out_grad, vocab=None,
+                      stream=None):
+    """cg_distill_topk_grad: distill_topk's gradient alone, from the lse it wrote."""
+    import torch
+    L = _row_lib()
+    B, V, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
+    g, gs = _grad_arg(out_grad, logits, B, V)
+    _row_call(L.cg_distill_topk_grad, logits, stream, *args, _row_arg(lse, torch.float32, "lse", logits, (B,)),
+              _row_arg(weight, torch.float32, "weight", logits, (B,)), g, gs)
+
+
+_distill_fn = None
+
+
+def _distill_function():
+    """The autograd function behind distill_topk_loss (torch is imported only when a call needs it)."""
+    global _distill_fn
+    if _distill_fn is None:
+        import torch
+
+        class DistillTopK(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, logits, mask, teacher_ids, teacher_logits, temperature, vocab):
+                rows = logits.shape[0]
+                loss = torch.empty(rows, dtype=torch.float32, device=logits.device)
+                lse = torch.empty_like(loss)
+                distill_topk(logits, mask, teacher_ids, teacher_logits, temperature, loss, lse, vocab=vocab)
+                ctx.save_for_backward(logits, mask, teacher_ids, teacher_logits, lse)
+                ctx.temperature, ctx.vocab = temperature, vocab
+                return loss
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, weight):
+                logits, mask, teacher_ids, teacher_logits, lse = ctx.saved_tensors
+                whole = ctx.vocab is None or ctx.vocab == logits.shape[1]
+                grad = (torch.empty if whole else torch.zeros)(logits.shape, dtype=logits.dtype, device=logits.device)
+                distill_topk_grad(logits, mask, teacher_ids, teacher_logits, ctx.temperature, lse,
+                                  weight.float().contiguous(), grad, vocab=ctx.vocab)
+                return grad, None, None, None, None, None
+
+        _distill_fn = DistillTopK
+    return _distill_fn
+
+
+def distill_topk_loss(logits, teacher_ids, teacher_logits, mask=None, temperature=1.0, vocab=None):
+    """The per-position losses of cg_distill_topk, differentiable by the
+    logits: logits [..., >= vocab], teacher_ids and teacher_logits [..., k],
+    mask [..., W] or None; float32 losses of the leading shape."""
+    lead = logits.shape[:-1]
+    x = logits.reshape(-1, logits.shape[-1])
+    if x.stride(-1) != 1:
+        x = x.contiguous()
+    ids = teacher_ids.reshape(-1, teacher_ids.shape[-1]).contiguous()
+    top = teacher_logits.reshape(-1, teacher_logits.shape[-1]).contiguous()
+    if mask is not None:
+        mask = mask.reshape(-1, mask.shape[-1]).contiguous()
+    for t, n in ((teacher_ids, "teacher_ids"), (teacher_logits, "teacher_logits")) + \
+            (((mask, "mask"),) if mask is not None else ()):
+        if t.reshape(-1, t.shape[-1]).shape[0] != x.shape[0]:
+            raise ValueError(f"{n} must have the logits' leading shape")
+    return _distill_function().apply(x, mask, ids, top, temperature, vocab).reshape(lead)

@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libcg.so")
 ARCH = os.environ.get("CG_OFFLOAD_ARCH", "gfx950")
-SOURCES = ["compiler.cpp", "capi.cpp", "contract.cpp", "pda.hip", "sample.hip"]
+SOURCES = ["compiler.cpp", "capi.cpp", "contract.cpp", "pda.hip", "sample.hip", "filter.hip", "top.hip", "distill.hip"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "-Wall", "--offload-arch=" + ARCH,
          # keep hipcc from emitting packed fp32 instructions
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
@@ -39,7 +39,7 @@ def build(verbose: bool = False) -> str:
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=3) as ex:
+    with ThreadPoolExecutor(max_workers=6) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     tmp = OUT + ".tmp%d" % os.getpid()
     cmd = [cc, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-Wl,--no-undefined", "-o", tmp] + objs

@@ -1,0 +1,160 @@
+// filter.hip -- gfx950 kernel of the filtered draw: temperature, top-k,
+// top-p and min-p over a masked row, then the inverse of the cumulative
+// weight at a given uniform number ("Constrained decoding", "The guarantee":
+// sampling runs after masking, so no sampling strategy can escape it).
+//
+//   k_filter_sample   one workgroup per row
+#include <algorithm>
+
+#include "cg_internal.hpp"
+#include "row_select.hpp"
+
+namespace cg {
+
+namespace {
+
+struct FilterArgs {
+    const void *logits;
+    int64_t stride;
+    const uint64_t *mask;
+    int wpr, V;
+    const float *temp;
+    const int32_t *top_k;
+    const float *top_p, *min_p, *uniform;
+    int32_t *ids;
+    float *logprob;
+};
+
+// Every filter keeps a prefix of the row's order (row_select.hpp), so the
+// kept set is a place: all candidates of larger keys than `key`, and the
+// first `ties` of those equal to it.
+struct Cut {
+    uint32_t key, ties;
+};
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void k_filter_sample(FilterArgs a) {
+    __shared__ SelectShared sh;
+    const int r = blockIdx.x;
+    RowView<DT> row{(const char *)a.logits + (size_t)r * (size_t)a.stride * (DT == 0 ? 4 : 2),
+                    a.mask ? a.mask + (size_t)r * a.wpr : nullptr, a.V};
+    const float T = a.temp[r];
+    const bool greedy = !(T > 0.f);
+    const uint32_t best = row_max_key(row, sh);
+    if (best == 0) {
+        if (threadIdx.x == 0) {
+            a.ids[r] = -1;
+            a.logprob[r] = 0.f;
+        }
+        return;
+    }
+    const Weight weight{(double)value_of_key(best), greedy ? 1.0 : 1.0 / (double)T};
+    const int k = a.top_k ? a.top_k[r] : 0;
+    const float p = a.top_p ? a.top_p[r] : 1.f;
+    const float mp = a.min_p ? a.min_p[r] : 0.f;
+
+    Cut cut{0, 0};  // below every candidate: all kept
+    uint64_t mass;
+    uint32_t pick_key = best, pick_n = 0;
+    if (greedy) {
+        mass = row_mass(row, weight, 0u, sh);
+    } else {
+        if (k > 0 && k < a.V) {
+            const Place q = row_find<DT, false>(row, weight, (uint32_t)k - 1, 0, sh);
+            const uint32_t ties = min(q.count, (uint32_t)k - q.above);
+            cut = Cut{q.key, ties};
+            mass = q.mass_above + ties * fixed_mass(weight(value_of_key(q.key)));
+        } else {
+            mass = row_mass(row, weight, 0u, sh);
+        }
+        if (p < 1.f) {
+            // rank j stays while the mass before it is under p * mass: the
+            // last one kept is the first whose own end reaches it
+            const uint64_t goal = p > 0.f ? (uint64_t)ceil((double)p * (double)mass) : 0;
+            if (goal == 0) {
+                cut = Cut{best, 1};
+                mass = fixed_mass(1.0);
+            } else {
+                const Place q = row_find<DT, true>(row, weight, 0, goal - 1, sh);
+                const uint64_t f = fixed_mass(weight(value_of_key(q.key)));
+                uint32_t ties = q.count;
+                if (f) ties = (uint32_t)min((uint64_t)ties, (goal - q.mass_above + f - 1) / f);
+                const Cut c{q.key, max(ties, 1u)};
+                if (c.key > cut.key || (c.key == cut.key && c.ties < cut.ties)) {
+                    cut = c;
+                    mass = q.mass_above + c.ties * f;
+                }
+            }
+        }
+        if (mp > 0.f) {
+            // the least key whose weight reaches min_p (weights rise with the key)
+            uint32_t lo = key_of_bits(0xFF7FFFFFu), hi = best;
+            const double least = fmin((double)mp, 1.0);
+            while (lo < hi) {
+                const uint32_t mid = lo + (hi - lo) / 2;
+                if (weight(value_of_key(mid)) >= least) hi = mid;
+                else lo = mid + 1;
+            }
+            if (lo > cut.key) {
+                cut = Cut{lo, 0xFFFFFFFFu};
+                mass = row_mass(row, weight, lo, sh);
+            }
+        }
+        const double u = (double)a.uniform[r];
+        const uint64_t at = u > 0.0 ? (uint64_t)fmin(u * (double)mass, (double)(mass - 1)) : 0;
+        const Place q = row_find<DT, true>(row, weight, 0, at, sh);
+        const uint64_t f = fixed_mass(weight(value_of_key(q.key)));
+        uint32_t n = q.count;
+        if (q.key == cut.key) n = min(n, cut.ties);
+        pick_key = q.key;
+        pick_n = f && at > q.mass_above ? (uint32_t)min((uint64_t)(n - 1), (at - q.mass_above) / f) : 0;
+    }
+    const int id = row_nth(row, pick_key, pick_n, sh);
+    if (threadIdx.x == 0) {
+        const float x = value_of_key(pick_key);
+        const double y = (double)x == weight.m ? 0.0 : ((double)x - weight.m) * weight.inv_t;
+        a.ids[r] = id;
+        a.logprob[r] = (float)(y - log((double)mass / kMassUnit));
+    }
+}
+
+}  // namespace
+
+}  // namespace cg
+
+using namespace cg;
+
+static int filter_arg_error(const char *msg) {
+    set_error("filter_sample: %s", msg);
+    return CG_E_ARG;
+}
+
+extern "C" {
+
+size_t cg_filter_workspace_bytes(int32_t batch, int32_t vocab) {
+    (void)batch;
+    (void)vocab;
+    return 0;
+}
+
+int cg_filter_sample(const void *d_logits, int32_t dtype, int32_t batch, int32_t vocab, int64_t row_stride,
+                     const uint64_t *d_mask, int32_t words_per_row, const float *d_temperature,
+                     const int32_t *d_top_k, const float *d_top_p, const float *d_min_p, const float *d_uniform,
+                     void *d_workspace, int32_t *d_out_ids, float *d_out_logprob, void *stream) {
+    if (dtype != 0 && dtype != 1) return filter_arg_error("dtype must be 0 (float32) or 1 (bfloat16)");
+    if (batch < 0 || vocab < 1 || vocab > CG_MAX_ROW_VOCAB) return filter_arg_error("bad batch / vocab");
+    if (row_stride < vocab) return filter_arg_error("row_stride < vocab");
+    if (d_mask && words_per_row < (vocab + 63) / 64) return filter_arg_error("words_per_row < ceil(vocab / 64)");
+    if (batch == 0) return CG_OK;
+    if (!d_logits || !d_temperature || !d_uniform || !d_out_ids || !d_out_logprob)
+        return filter_arg_error("NULL device pointer");
+    (void)d_workspace;
+    const FilterArgs a{d_logits, row_stride, d_mask, words_per_row, vocab, d_temperature,
+                       d_top_k,  d_top_p,    d_min_p, d_uniform,    d_out_ids, d_out_logprob};
+    if (dtype == 0)
+        hipLaunchKernelGGL((k_filter_sample<0>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
+    else
+        hipLaunchKernelGGL((k_filter_sample<1>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
+    return launch_status("filter_sample");
+}
+
+}  // extern "C"

@@ -1,0 +1,132 @@
+// top.hip -- gfx950 kernel of a masked row's k largest logits and its
+// log-normaliser: what a teacher records at every position, and the top
+// log-probabilities of a reply.
+//
+//   k_top_logits   one workgroup per row
+#include <algorithm>
+
+#include "cg_internal.hpp"
+#include "row_select.hpp"
+
+namespace cg {
+
+namespace {
+
+struct TopArgs {
+    const void *logits;
+    int64_t stride;
+    const uint64_t *mask;
+    int wpr, V, k;
+    int32_t *ids;
+    float *top, *lse;
+};
+
+// Sorts list[0, n) falling; n a power of two, every thread calls it.
+__device__ void sort_falling(uint64_t *list, int n) {
+    for (int size = 2; size <= n; size <<= 1) {
+        for (int step = size >> 1; step; step >>= 1) {
+            __syncthreads();
+            for (int t = threadIdx.x; t < n / 2; t += kRowThreads) {
+                const int lo = 2 * t - (t & (step - 1)), hi = lo + step;
+                const uint64_t a = list[lo], b = list[hi];
+                const bool falling = (lo & size) == 0;
+                if (falling ? a < b : a > b) {
+                    list[lo] = b;
+                    list[hi] = a;
+                }
+            }
+        }
+    }
+    __syncthreads();
+}
+
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void k_top_logits(TopArgs a) {
+    __shared__ SelectShared sh;
+    __shared__ uint64_t list[CG_MAX_TOP];  // key in the high half, the id's complement in the low: one order
+    __shared__ uint32_t n_list;
+    const int r = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    RowView<DT> row{(const char *)a.logits + (size_t)r * (size_t)a.stride * (DT == 0 ? 4 : 2),
+                    a.mask ? a.mask + (size_t)r * a.wpr : nullptr, a.V};
+    int n_pow = 1;
+    while (n_pow < a.k) n_pow <<= 1;
+    for (int i = threadIdx.x; i < n_pow; i += kRowThreads) list[i] = 0;
+    if (threadIdx.x == 0) n_list = 0;
+    const uint32_t best = row_max_key(row, sh);
+    uint64_t mass = 0;
+    if (best) {
+        const Weight weight{(double)value_of_key(best), 1.0};
+        mass = row_mass(row, weight, 0u, sh);
+        const Place q = row_find<DT, false>(row, weight, (uint32_t)a.k - 1, 0, sh);
+        const uint32_t ties = min(q.count, (uint32_t)a.k - q.above);
+        // larger keys in any order, the ties by rising id until enough
+        uint32_t before = 0;
+        for (int base = 0; base < row.V; base += kRowThreads) {
+            const int i = base + threadIdx.x;
+            const uint32_t key = i < row.V ? row.key(i) : 0u;
+            if (key > q.key) list[atomicAdd(&n_list, 1u)] = ((uint64_t)key << 32) | (uint32_t)~i;
+            const uint64_t hits = __ballot(key == q.key);
+            if (lane == 0) sh.wave[wave] = __popcll(hits);
+            __syncthreads();
+            uint32_t mine = before;
+            for (int w = 0; w < kRowWaves; w++) {
+                if (w < wave) mine += sh.wave[w];
+                before += sh.wave[w];
+            }
+            mine += __popcll(hits & ((1ull << lane) - 1));
+            if (key == q.key && mine < ties) list[q.above + mine] = ((uint64_t)key << 32) | (uint32_t)~i;
+            __syncthreads();
+        }
+        sort_falling(list, n_pow);
+        if (threadIdx.x == 0) a.lse[r] = (float)(weight.m + log((double)mass / kMassUnit));
+    } else if (threadIdx.x == 0) {
+        a.lse[r] = -INFINITY;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.k; i += kRowThreads) {
+        const uint64_t e = list[i];
+        a.ids[(size_t)r * a.k + i] = e ? (int32_t)~(uint32_t)e : -1;
+        a.top[(size_t)r * a.k + i] = e ? value_of_key((uint32_t)(e >> 32)) : -INFINITY;
+    }
+}
+
+}  // namespace
+
+}  // namespace cg
+
+using namespace cg;
+
+static int top_arg_error(const char *msg) {
+    set_error("top_logits: %s", msg);
+    return CG_E_ARG;
+}
+
+extern "C" {
+
+size_t cg_top_workspace_bytes(int32_t batch, int32_t vocab, int32_t k) {
+    (void)batch;
+    (void)vocab;
+    (void)k;
+    return 0;
+}
+
+int cg_top_logits(const void *d_logits, int32_t dtype, int32_t batch, int32_t vocab, int64_t row_stride,
+                  const uint64_t *d_mask, int32_t words_per_row, int32_t k, void *d_workspace, int32_t *d_out_ids,
+                  float *d_out_logits, float *d_out_lse, void *stream) {
+    if (dtype != 0 && dtype != 1) return top_arg_error("dtype must be 0 (float32) or 1 (bfloat16)");
+    if (batch < 0 || vocab < 1 || vocab > CG_MAX_ROW_VOCAB) return top_arg_error("bad batch / vocab");
+    if (k < 1 || k > CG_MAX_TOP) return top_arg_error("k out of range");
+    if (row_stride < vocab) return top_arg_error("row_stride < vocab");
+    if (d_mask && words_per_row < (vocab + 63) / 64) return top_arg_error("words_per_row < ceil(vocab / 64)");
+    if (batch == 0) return CG_OK;
+    if (!d_logits || !d_out_ids || !d_out_logits || !d_out_lse) return top_arg_error("NULL device pointer");
+    (void)d_workspace;
+    const TopArgs a{d_logits, row_stride, d_mask, words_per_row, vocab, k, d_out_ids, d_out_logits, d_out_lse};
+    if (dtype == 0)
+        hipLaunchKernelGGL((k_top_logits<0>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
+    else
+        hipLaunchKernelGGL((k_top_logits<1>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
+    return launch_status("top_logits");
+}
+
+}  // extern "C"

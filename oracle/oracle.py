@@ -771,6 +771,119 @@ def unpack_mask(words, V):
 
 
 # ---------------------------------------------------------------------------
+# Row operators over masked logits, one row at a time in float64: the draw
+# with top-k, top-p and min-p from a given uniform number, the k largest
+# logits, the loss against a teacher's top logits with its gradient.
+# ---------------------------------------------------------------------------
+
+def ranked(x, allowed=None):
+    """Ids of a row's candidates (allowed, above -inf, not NaN) by falling
+    logit, equal logits by rising id."""
+    x = np.asarray(x, dtype=np.float64)
+    ok = x > -np.inf  # false for NaN
+    if allowed is not None:
+        ok &= np.asarray(allowed, dtype=bool)
+    ids = np.flatnonzero(ok)
+    return ids[np.argsort(-x[ids], kind="stable")]
+
+
+def filter_sample_row(x, allowed, T, k, p, mp, u):
+    """(id, logprob, margin): the pick of the first kept rank up to which the
+    weights sum to more than u S; k, p, mp may be None.  margin: how near the
+    nearest comparison between masses came to a tie, as a share of the mass
+    compared."""
+    x = np.asarray(x, dtype=np.float64)
+    order = ranked(x, allowed)
+    if not len(order):
+        return -1, 0.0, math.inf
+    v = x[order]
+    T = float(np.float32(T))
+    greedy = not T > 0
+    with np.errstate(invalid="ignore", over="ignore"):
+        y = np.where(v == v[0], 0.0, (v - v[0]) / (1.0 if greedy else T))
+    y = np.where(np.isnan(y), -np.inf, y)
+    w = np.exp(y)
+    if greedy:
+        return int(order[0]), -math.log(math.fsum(w)), math.inf
+    margin = math.inf
+    n = len(order)
+    if k is not None and 0 < k < n:
+        n = int(k)
+    if p is not None and float(np.float32(p)) < 1:
+        p = float(np.float32(p))
+        total = math.fsum(w[:n])
+        before = np.concatenate([[0.0], np.cumsum(w[:n])[:-1]])
+        keep = before < p * total
+        keep[0] = True
+        if n > 1:
+            margin = min(margin, float(np.min(np.abs(before[1:] - p * total))) / total)
+        n = int(keep.sum())
+    if mp is not None and float(np.float32(mp)) > 0:
+        mp = min(float(np.float32(mp)), 1.0)
+        margin = min(margin, float(np.min(np.abs(np.where(w == 1.0, np.inf, w) - mp))) / mp)
+        n = min(n, max(1, int((w >= mp).sum())))
+    upto = np.cumsum(w[:n])
+    S = upto[-1]
+    u = float(np.float32(u))
+    u = u if u > 0 else 0.0
+    if u > 0 and n > 1:
+        margin = min(margin, float(np.min(np.abs(upto[:-1] - u * S))) / S)
+    j = int(np.searchsorted(upto, u * S, side="right"))
+    j = min(j, int((w[:n] > 0).sum()) - 1)
+    return int(order[j]), float(y[j] - math.log(math.fsum(w[:n]))), margin
+
+
+def top_logits_row(x, allowed, k):
+    """(ids, logits, lse) of the first k ranks, padded with -1 and -inf."""
+    x = np.asarray(x, dtype=np.float64)
+    order = ranked(x, allowed)
+    ids = np.full(k, -1, dtype=np.int64)
+    top = np.full(k, -np.inf)
+    m = min(k, len(order))
+    ids[:m] = order[:m]
+    top[:m] = x[order[:m]]
+    if not len(order):
+        return ids, top, -math.inf
+    v = x[order]
+    with np.errstate(invalid="ignore"):
+        lse = float(v[0] + np.log(np.sum(np.where(v == v[0], 1.0, np.exp(v - v[0])))))
+    return ids, top, lse
+
+
+def distill_row(x, allowed, ids, t, tau):
+    """(loss, lse, gradient) of one row: tau^2 KL(p || q) with q the masked
+    softmax of x / tau and p the softmax of t / tau over the entries q can
+    take; the gradient by x."""
+    x = np.asarray(x, dtype=np.float64)
+    tau = float(np.float32(tau))
+    ok = ~(x == -np.inf)  # a NaN stays and spreads
+    if allowed is not None:
+        ok &= np.asarray(allowed, dtype=bool)
+    grad = np.zeros(len(x))
+    use = np.flatnonzero(ok)
+    if not len(use):
+        return 0.0, -math.inf, grad
+    z = x[use] / tau
+    m = np.max(z)  # logits at a type's lowest value: differences before sums
+    logsum = float(np.log(np.sum(np.exp(z - m))))
+    lse = float(m + logsum)
+    ids = np.asarray(ids, dtype=np.int64)
+    t = np.asarray(t, dtype=np.float64)
+    has = (ids >= 0) & (ids < len(x)) & (t > -np.inf)
+    has[has] = ok[ids[has]]
+    if not has.any():
+        return 0.0, lse, grad
+    ids, t = ids[has], t[has] / tau
+    logp = t - np.max(t)
+    logp -= np.log(np.sum(np.exp(logp)))
+    p = np.exp(logp)
+    loss = tau * tau * float(np.sum(np.where(p > 0, p * (logp - (x[ids] / tau - m) + logsum), 0.0)))
+    grad[use] = np.exp(z - m - logsum)
+    np.subtract.at(grad, ids, p)
+    return loss, lse, tau * grad
+
+
+# ---------------------------------------------------------------------------
 # Calc-span evaluator: exact integers, * and / before + and -, left to
 # right, / truncating toward zero, division by zero an error (page "Evaluator
 # aware decoding", sections "The core idea" and "A concrete prototype on
