@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "cg_internal.hpp"
+#include "row_hist.hpp"
 #include "row_select.hpp"
 
 namespace cg {
@@ -117,6 +118,111 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_sample(FilterArgs a) {
     }
 }
 
+// bfloat16 rows: one read, the filters on the counts of the row's values
+// (row_hist.hpp).
+template <int NP, bool VEC>
+__global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
+    __shared__ HistShared sh;
+    const int r = blockIdx.x, lane = threadIdx.x & 63;
+    HistRow<NP, VEC> row;
+    row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
+             a.wpr, a.V);
+    const float T = a.temp[r];
+    const int k = a.top_k ? a.top_k[r] : 0;
+    const float p = a.top_p ? a.top_p[r] : 1.f;
+    const float mp = a.min_p ? a.min_p[r] : 0.f;
+    const float u = a.uniform[r];
+    const bool greedy = !(T > 0.f);
+    HistOrder<NP, VEC> order(sh, row);
+    if (!order.build(greedy ? 1.0 : 1.0 / (double)T)) {
+        if (threadIdx.x == 0) {
+            a.ids[r] = -1;
+            a.logprob[r] = 0.f;
+        }
+        return;
+    }
+    const uint32_t top = order.top_pos();
+    double mass = order.total_mass();
+    uint32_t pos = top, n = 0, count;
+    if (greedy) {
+        count = order.template find<0>(0, 0.0).count;
+    } else {
+        uint32_t cut = 0xFFFFFFFFu, ties = 0;  // the last kept position, and how many of it stay
+        if (k > 0 && (uint32_t)k < order.total_count()) {
+            const HistPlace q = order.template find<0>((uint32_t)k - 1, 0.0);
+            cut = q.pos;
+            ties = (uint32_t)k - q.above;
+            mass = q.mass_above + ties * q.w;
+        }
+        if (p < 1.f) {
+            // rank j stays while the mass before it is under p * mass: the
+            // last one kept is the first whose own end reaches it
+            if (p <= 0.f) {
+                cut = top;
+                ties = 1;
+                mass = 1.0;
+            } else {
+                const double goal = (double)p * mass;
+                const HistPlace q = order.template find<2>(0, goal);
+                const uint32_t keep =
+                    min(q.count, (uint32_t)fmin(fmax(ceil((goal - q.mass_above) / q.w), 1.0), 4294967040.0));
+                if (q.pos < cut || (q.pos == cut && keep < ties)) {
+                    cut = q.pos;
+                    ties = keep;
+                    mass = q.mass_above + ties * q.w;
+                }
+            }
+        }
+        if (mp > 0.f) {
+            // the last position whose weight reaches min_p (weights fall with
+            // the position): 64 points of the range at a time
+            const double least = fmin((double)mp, 1.0);
+            uint32_t lo = top, hi = 32768u + (uint32_t)kInfIdx;  // holds at lo, not at hi (-inf)
+            while (hi - lo > 1) {
+                const uint32_t step = (hi - lo + 63) / 64, at = min(lo + (uint32_t)lane * step, hi);
+                const uint64_t ok = __ballot(at < hi && order.weight(bits_value(pos_bits(at))) >= least);
+                const int l = 63 - __builtin_clzll(ok);  // lane 0 holds
+                lo = lo + (uint32_t)l * step;
+                hi = min(lo + step, hi);
+            }
+            if (lo < cut) {
+                cut = lo;
+                ties = 0xFFFFFFFFu;
+                mass = order.mass_to(lo);
+            }
+        }
+        const double at = u > 0.f ? fmin((double)u, 1.0 - 0x1p-53) * mass : 0.0;
+        HistPlace q = order.template find<1>(0, at);
+        uint32_t left = q.count;
+        if (q.pos >= cut) {
+            if (q.pos > cut) q = order.template find<1>(0, mass * (1.0 - 0x1p-50));
+            left = min(q.count, ties);
+        }
+        pos = q.pos;
+        count = q.count;
+        const double j = floor((at - q.mass_above) / q.w);
+        n = j > 0.0 ? min((uint32_t)fmin(j, 4294967040.0), left - 1) : 0u;
+    }
+    const int id = row.nth(pos, count, n, sh);
+    if (threadIdx.x == 0) {
+        const double x = (double)bits_value(pos_bits(pos));
+        const double y = x == order.weight.m ? 0.0 : (x - order.weight.m) * order.weight.inv_t;
+        a.ids[r] = id;
+        a.logprob[r] = (float)(y - log(mass));
+    }
+}
+
+// Pieces of 8 ids a thread holds (row_hist.hpp): as many as the row needs, up
+// to 128 registers' worth beside what the kernel works with; longer rows are
+// taken in spans.
+template <bool VEC>
+void launch_counts(const FilterArgs &a, int batch, hipStream_t st) {
+    const int pieces = (a.V + kPieceIds - 1) / kPieceIds;
+    if (pieces <= 4) hipLaunchKernelGGL((k_filter_counts<4, VEC>), dim3(batch), dim3(kRowThreads), 0, st, a);
+    else if (pieces <= 8) hipLaunchKernelGGL((k_filter_counts<8, VEC>), dim3(batch), dim3(kRowThreads), 0, st, a);
+    else hipLaunchKernelGGL((k_filter_counts<kMaxPieces, VEC>), dim3(batch), dim3(kRowThreads), 0, st, a);
+}
+
 }  // namespace
 
 }  // namespace cg
@@ -150,10 +256,12 @@ int cg_filter_sample(const void *d_logits, int32_t dtype, int32_t batch, int32_t
     (void)d_workspace;
     const FilterArgs a{d_logits, row_stride, d_mask, words_per_row, vocab, d_temperature,
                        d_top_k,  d_top_p,    d_min_p, d_uniform,    d_out_ids, d_out_logprob};
-    if (dtype == 0)
+    if (dtype == 0) {
         hipLaunchKernelGGL((k_filter_sample<0>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
-    else
-        hipLaunchKernelGGL((k_filter_sample<1>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
+    } else {
+        if ((uintptr_t)d_logits % 16 == 0 && row_stride % 8 == 0) launch_counts<true>(a, batch, (hipStream_t)stream);
+        else launch_counts<false>(a, batch, (hipStream_t)stream);
+    }
     return launch_status("filter_sample");
 }
 
