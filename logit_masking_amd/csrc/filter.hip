@@ -120,11 +120,11 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_sample(FilterArgs a) {
 
 // bfloat16 rows: one read, the filters on the counts of the row's values
 // (row_hist.hpp).
-template <int NP, bool VEC>
+template <int NP>
 __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     __shared__ HistShared sh;
     const int r = blockIdx.x, lane = threadIdx.x & 63;
-    HistRow<NP, VEC> row;
+    HistRow<NP> row;
     row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
              a.wpr, a.V);
     const float T = a.temp[r];
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     const float mp = a.min_p ? a.min_p[r] : 0.f;
     const float u = a.uniform[r];
     const bool greedy = !(T > 0.f);
-    HistOrder<NP, VEC> order(sh, row);
+    HistOrder<NP> order(sh, row);
     if (!order.build(greedy ? 1.0 : 1.0 / (double)T)) {
         if (threadIdx.x == 0) {
             a.ids[r] = -1;
@@ -215,12 +215,11 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
 // Pieces of 8 ids a thread holds (row_hist.hpp): as many as the row needs, up
 // to 128 registers' worth beside what the kernel works with; longer rows are
 // taken in spans.
-template <bool VEC>
 void launch_counts(const FilterArgs &a, int batch, hipStream_t st) {
-    const int pieces = (a.V + kPieceIds - 1) / kPieceIds;
-    if (pieces <= 4) hipLaunchKernelGGL((k_filter_counts<4, VEC>), dim3(batch), dim3(kRowThreads), 0, st, a);
-    else if (pieces <= 8) hipLaunchKernelGGL((k_filter_counts<8, VEC>), dim3(batch), dim3(kRowThreads), 0, st, a);
-    else hipLaunchKernelGGL((k_filter_counts<kMaxPieces, VEC>), dim3(batch), dim3(kRowThreads), 0, st, a);
+    const int pieces = (a.V + 7 + kPieceIds - 1) / kPieceIds;  // 7: the largest skew
+    if (pieces <= 4) hipLaunchKernelGGL((k_filter_counts<4>), dim3(batch), dim3(kRowThreads), 0, st, a);
+    else if (pieces <= 8) hipLaunchKernelGGL((k_filter_counts<8>), dim3(batch), dim3(kRowThreads), 0, st, a);
+    else hipLaunchKernelGGL((k_filter_counts<kMaxPieces>), dim3(batch), dim3(kRowThreads), 0, st, a);
 }
 
 }  // namespace
@@ -259,8 +258,7 @@ int cg_filter_sample(const void *d_logits, int32_t dtype, int32_t batch, int32_t
     if (dtype == 0) {
         hipLaunchKernelGGL((k_filter_sample<0>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
     } else {
-        if ((uintptr_t)d_logits % 16 == 0 && row_stride % 8 == 0) launch_counts<true>(a, batch, (hipStream_t)stream);
-        else launch_counts<false>(a, batch, (hipStream_t)stream);
+        launch_counts(a, batch, (hipStream_t)stream);
     }
     return launch_status("filter_sample");
 }

@@ -90,14 +90,16 @@ struct HistPlace {
 };
 
 // The row: NP pieces a thread held in registers; rows longer than NP pieces
-// are taken in spans of NP.  VEC: 16-byte aligned rows.
-template <int NP, bool VEC>
+// are taken in spans of NP.  Every load is 16 bytes from a 16-byte boundary:
+// a row that starts past one by `skew` ids is taken from the boundary, the
+// ids before its own start never allowed.
+template <int NP>
 struct HistRow {
     static constexpr int kSpan = NP * kPieceIds;
     __amdgpu_buffer_rsrc_t rx, rm;
     const uint16_t *x;
     const uint64_t *mask;
-    int V, words;
+    int V, skew;
     uint32_t d[NP][4];
     int span_at;  // the span in the registers
 
@@ -105,16 +107,19 @@ struct HistRow {
         x = (const uint16_t *)logits;
         mask = m;
         V = vocab;
-        words = min(wpr, (vocab + 63) / 64);
-        rx = __builtin_amdgcn_make_buffer_rsrc((void *)logits, (short)0, (V * 2 + 3) & ~3, kBufWord3);
-        rm = __builtin_amdgcn_make_buffer_rsrc((void *)m, (short)0, m ? words * 8 : 0, kBufWord3);
+        skew = (int)(((uintptr_t)logits & 15) >> 1);
+        rx = __builtin_amdgcn_make_buffer_rsrc((void *)(x - skew), (short)0, ((V + skew) * 2 + 3) & ~3, kBufWord3);
+        rm = __builtin_amdgcn_make_buffer_rsrc((void *)m, (short)0, m ? (vocab + 63) / 64 * 8 : 0, kBufWord3);
     }
-    __device__ int spans() const { return NP < kMaxPieces ? 1 : (V + kSpan - 1) / kSpan; }
-    __device__ int first_id(int span, int p) const { return span * kSpan + p * kPieceIds + (int)threadIdx.x * 8; }
+    __device__ int spans() const { return NP < kMaxPieces ? 1 : (V + skew + kSpan - 1) / kSpan; }
+    __device__ int first_id(int span, int p) const {
+        return span * kSpan + p * kPieceIds + (int)threadIdx.x * 8 - skew;
+    }
 
     // Bit j: id first + j is in the row and allowed.
     __device__ __forceinline__ uint32_t allowed8(uint32_t byte, int first) const {
         const int left = V - first;
+        if (first < 0) byte &= 0xFFu << -first;
         return left >= 8 ? byte : left <= 0 ? 0u : byte & ((1u << left) - 1u);
     }
 
@@ -128,30 +133,26 @@ struct HistRow {
         const int base = span * kSpan;
         uint32_t mb[NP];
 #pragma unroll
-        for (int p = 0; p < NP; p++)
-            mb[p] = mask ? __builtin_amdgcn_raw_buffer_load_b8(rm, (base + p * kPieceIds) / 8 + (int)threadIdx.x, 0, 0)
-                         : 0xFFu;
+        for (int p = 0; p < NP; p++) {
+            mb[p] = 0xFFu;
+            if (mask) {
+                const int q = (base + p * kPieceIds) / 8 + (int)threadIdx.x;
+                mb[p] = __builtin_amdgcn_raw_buffer_load_b8(rm, q, 0, 0);
+                if (skew) mb[p] = (mb[p] << 8) | __builtin_amdgcn_raw_buffer_load_b8(rm, q - 1, 0, 0);
+            }
+        }
         while_waiting();
 #pragma unroll
         for (int p = 0; p < NP; p++) {
             const int first = first_id(span, p);
-            mb[p] = allowed8(mb[p], first);
-            if (VEC) {
-                const uint4 v = __builtin_bit_cast(
-                    uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, mb[p] ? first * 2 : 0x7FFFFFF0, 0, 0));
-                d[p][0] = v.x; d[p][1] = v.y; d[p][2] = v.z; d[p][3] = v.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const uint32_t lo = (mb[p] >> (2 * j)) & 1 ? x[first + 2 * j] : 0u;
-                    const uint32_t hi = (mb[p] >> (2 * j + 1)) & 1 ? x[first + 2 * j + 1] : 0u;
-                    d[p][j] = lo | (hi << 16);
-                }
-            }
+            mb[p] = allowed8(mask && skew ? (mb[p] >> (8 - skew)) & 0xFFu : mb[p], first);
+            const uint4 v = __builtin_bit_cast(
+                uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, mb[p] ? (first + skew) * 2 : 0x7FFFFFF0, 0, 0));
+            d[p][0] = v.x; d[p][1] = v.y; d[p][2] = v.z; d[p][3] = v.w;
         }
 #pragma unroll
         for (int p = 0; p < NP; p++) {
-            if (mask || base + (p + 1) * kPieceIds > V) {  // uniform
+            if (mask || skew || base + (p + 1) * kPieceIds > V) {  // uniform
                 const uint4 s = lut[mb[p]];
                 d[p][0] = (d[p][0] & s.x) | (~s.x & kNegInfPair);
                 d[p][1] = (d[p][1] & s.y) | (~s.y & kNegInfPair);
@@ -179,13 +180,86 @@ struct HistRow {
         }
     }
 
+    // Appends every candidate of position <= last to the list as (position,
+    // id), any order.  Its length (sh.n_list, zeroed by the caller) may pass
+    // `room`: what does not fit is dropped.
+    __device__ __forceinline__ void collect(uint32_t last, uint64_t *list, uint32_t room, HistShared &sh) {
+        typedef short s16x2 __attribute__((ext_vector_type(2)));
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        // positive down to bits b: as signed 16-bit numbers, at least b;
+        // negatives too: as unsigned ones, at most the last's bits (zeros:
+        // the negative one's).  Positive NaNs pass here and fail below.
+        const bool pos = last < 32767u;
+        const uint32_t b = last == 32767u ? 0x8000u : pos_bits(last);
+#pragma unroll
+        for (int p = 0; p < NP; p++) {
+            bool hit;
+            if (pos) {  // uniform
+                s16x2 m = __builtin_elementwise_max(__builtin_bit_cast(s16x2, d[p][0]), __builtin_bit_cast(s16x2, d[p][1]));
+                m = __builtin_elementwise_max(m, __builtin_elementwise_max(__builtin_bit_cast(s16x2, d[p][2]),
+                                                                           __builtin_bit_cast(s16x2, d[p][3])));
+                hit = max((int)m.x, (int)m.y) >= (int)b;
+            } else {
+                u16x2 m = __builtin_elementwise_min(__builtin_bit_cast(u16x2, d[p][0]), __builtin_bit_cast(u16x2, d[p][1]));
+                m = __builtin_elementwise_min(m, __builtin_elementwise_min(__builtin_bit_cast(u16x2, d[p][2]),
+                                                                           __builtin_bit_cast(u16x2, d[p][3])));
+                hit = min((uint32_t)m.x, (uint32_t)m.y) <= b;
+            }
+            if (hit) {
+                uint64_t lo = d[p][0] | ((uint64_t)d[p][1] << 32), hi = d[p][2] | ((uint64_t)d[p][3] << 32);
+                const int first = first_id(span_at, p);
+#pragma unroll 1
+                for (int j = 0; j < 8; j++) {
+                    const uint32_t v = (uint32_t)lo & 0xFFFFu;
+                    lo = (lo >> 16) | (hi << 48);
+                    hi >>= 16;
+                    const uint32_t at = v == 0x8000u ? 32767u : v < 0x8000u ? 32767u - v : v;
+                    if (at <= last && (v <= (uint32_t)kInfIdx || v >= 0x8000u)) {
+                        const uint32_t slot = atomicAdd(&sh.n_list, 1u);
+                        if (slot < room) list[slot] = ((uint64_t)at << 32) | (uint32_t)(first + j);
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // Calls take(rank, id) for the first `upto` candidates of position pos by
+    // rising id, reading the row again 1024 ids at a time.
+    template <class F>
+    __device__ void walk(uint32_t pos, uint32_t upto, HistShared &sh, F take) const {
+        const uint32_t bits = pos_bits(pos), same = bits == 0 ? 0x7FFFu : 0xFFFFu;  // the two zeros
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        uint32_t before = 0;
+        __syncthreads();
+        for (int base = 0; base < V && before < upto; base += kRowThreads) {  // uniform
+            const int i = base + (int)threadIdx.x;
+            const bool hit = i < V && (!mask || ((mask[i >> 6] >> (i & 63)) & 1)) && ((x[i] ^ bits) & same) == 0;
+            const uint64_t hits = __ballot(hit);
+            if (lane == 0) sh.w_cnt[wave] = __popcll(hits);
+            __syncthreads();
+            uint32_t mine = before;
+            for (int w = 0; w < kRowWaves; w++) {
+                const uint32_t c = sh.w_cnt[w];
+                mine += w < wave ? c : 0;
+                before += c;
+            }
+            mine += __popcll(hits & ((1ull << lane) - 1));
+            if (hit && mine < upto) take(mine, i);
+            __syncthreads();
+        }
+    }
+    // The first `upto` candidates of position pos, listed in order.
+    __device__ void first_of(uint32_t pos, uint32_t upto, uint64_t *list, HistShared &sh) const {
+        walk(pos, upto, sh, [&](uint32_t rank, int id) { list[rank] = ((uint64_t)pos << 32) | (uint32_t)id; });
+    }
+
     // The id of the n-th (from 0) of the row's `count` candidates of position
     // pos, by rising id.
     __device__ int nth(uint32_t pos, uint32_t count, uint32_t n, HistShared &sh) {
         const uint32_t bits = pos_bits(pos);
         const uint32_t same = bits == 0 ? 0x7FFF7FFFu : 0xFFFFFFFFu;  // the two zeros
         const uint32_t want = bits | (bits << 16);
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         uint32_t *list = sh.blk_cnt;  // no longer needed
         // match bits of a piece
         auto match = [&](int p) -> uint32_t {
@@ -228,44 +302,28 @@ struct HistRow {
             __syncthreads();
             return sh.found;
         }
-        // many: walk the row again, 1024 ids at a time
-        uint32_t before = 0;
+        // many: walk the row again
         if (threadIdx.x == 0) sh.found = -1;
-        __syncthreads();
-        for (int base = 0; base < V; base += kRowThreads) {
-            const int i = base + (int)threadIdx.x;
-            const bool hit = i < V && (!mask || ((mask[i >> 6] >> (i & 63)) & 1)) && ((x[i] ^ bits) & same & 0xFFFFu) == 0;
-            const uint64_t hits = __ballot(hit);
-            if (lane == 0) sh.w_cnt[wave] = __popcll(hits);
-            __syncthreads();
-            uint32_t mine = before;
-            for (int w = 0; w < kRowWaves; w++) {
-                const uint32_t c = sh.w_cnt[w];
-                mine += w < wave ? c : 0;
-                before += c;
-            }
-            mine += __popcll(hits & ((1ull << lane) - 1));
-            if (hit && mine == n) sh.found = i;
-            __syncthreads();
-            if (before > n) break;  // uniform
-        }
+        walk(pos, n + 1, sh, [&](uint32_t rank, int id) {
+            if (rank == n) sh.found = id;
+        });
         return sh.found;
     }
 };
 
 // The counted row: totals by block, and the searches.  Every wave runs the
 // searches alike, so no result is handed over.
-template <int NP, bool VEC>
+template <int NP>
 struct HistOrder {
     HistShared &sh;
-    HistRow<NP, VEC> &row;
+    HistRow<NP> &row;
     Weight weight;
     int wide;  // -1: h holds both signs in 16 bits; 0 / 1: that sign in 32 bits
     // lane w < 16: candidates and mass before, and up to the end of, the 64 blocks of w
     uint32_t w_above, w_incl;
     double w_mass_above, w_mass_incl;
 
-    __device__ __forceinline__ HistOrder(HistShared &s, HistRow<NP, VEC> &r) : sh(s), row(r) {}
+    __device__ __forceinline__ HistOrder(HistShared &s, HistRow<NP> &r) : sh(s), row(r) {}
 
     static __device__ __forceinline__ void clear(HistShared &sh) {
         uint4 *h = (uint4 *)sh.h;
@@ -324,7 +382,7 @@ struct HistOrder {
         uint32_t pg, ng;
         survey(pg, ng, true);
         __syncthreads();
-        if (sh.counted != (uint32_t)n_spans * (uint32_t)HistRow<NP, VEC>::kSpan) {
+        if (sh.counted != (uint32_t)n_spans * (uint32_t)HistRow<NP>::kSpan) {
             // a count overflowed
             if (t == 0) sh.top_pos = 0xFFFFFFFFu;
             for (int sign = 0; sign < 2; sign++) {
@@ -364,6 +422,7 @@ struct HistOrder {
         w_mass_above = from_left(w_mass_incl);
         return true;
     }
+    // (These read other lanes: every lane calls them.)
     __device__ uint32_t top_pos() const { return top_pos_; }
     __device__ double total_mass() const { return lane_double(w_mass_incl, kRowWaves - 1); }
     __device__ uint32_t total_count() const { return (uint32_t)lane_int((int)w_incl, kRowWaves - 1); }

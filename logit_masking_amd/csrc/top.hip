@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "cg_internal.hpp"
+#include "row_hist.hpp"
 #include "row_select.hpp"
 
 namespace cg {
@@ -90,6 +91,94 @@ __global__ __launch_bounds__(kRowThreads) void k_top_logits(TopArgs a) {
     }
 }
 
+// Room of the candidates' list: k and the ties of the k-th.
+constexpr uint32_t kListRoom = 2048;
+static_assert(CG_MAX_TOP < kListRoom && kListRoom * 8 <= sizeof(uint32_t) * kHistDwords, "the list lies over the counts");
+
+// Writes the first k of the n listed candidates in rising order of their
+// entries (position, id).
+template <class VALUE>
+__device__ void write_top(uint64_t *list, uint32_t n, const TopArgs &a, int r, VALUE value) {
+    int32_t *ids = a.ids + (size_t)r * a.k;
+    float *top = a.top + (size_t)r * a.k;
+    auto put = [&](uint32_t rank, uint64_t e) {
+        if (rank < (uint32_t)a.k) {
+            ids[rank] = (int32_t)(uint32_t)e;
+            top[rank] = value((uint32_t)(e >> 32));
+        }
+    };
+    if (n <= 512) {
+        // each entry's rank is the number of smaller ones: no barrier, every
+        // read a broadcast (sorting 512 takes 45 barriers)
+        if (threadIdx.x < n) {
+            const uint64_t e = list[threadIdx.x];
+            uint32_t rank = 0;
+#pragma unroll 8
+            for (uint32_t i = 0; i < n; i++) rank += list[i] < e;
+            put(rank, e);
+        }
+    } else {
+        int n_pow = 1024;
+        while ((uint32_t)n_pow < n) n_pow <<= 1;
+        for (uint32_t i = threadIdx.x; i < n; i += kRowThreads) list[i] = ~list[i];
+        for (uint32_t i = n + threadIdx.x; i < (uint32_t)n_pow; i += kRowThreads) list[i] = 0;
+        sort_falling(list, n_pow);
+        for (uint32_t i = threadIdx.x; i < min(n, (uint32_t)a.k); i += kRowThreads) put(i, ~list[i]);
+    }
+    for (uint32_t i = n + threadIdx.x; i < (uint32_t)a.k; i += kRowThreads) {
+        ids[i] = -1;
+        top[i] = -INFINITY;
+    }
+}
+
+// bfloat16 rows: one read, the k-th value from the counts (row_hist.hpp),
+// then the candidates down to it from the registers.
+template <int NP>
+__global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
+    __shared__ HistShared sh;
+    const int r = blockIdx.x;
+    HistRow<NP> row;
+    row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
+             a.wpr, a.V);
+    HistOrder<NP> order(sh, row);
+    uint64_t *list = (uint64_t *)sh.h;
+    uint32_t n = 0;
+    if (order.build(1.0)) {
+        const HistPlace q = order.template find<0>((uint32_t)a.k - 1, 0.0);
+        const double mass = order.total_mass();
+        if (threadIdx.x == 0) a.lse[r] = (float)(order.weight.m + log(mass));
+        // every tie of the last value when they fit, else only the larger
+        // candidates here and as many ties as are wanted by their ids
+        const bool all = q.above + q.count <= kListRoom;
+        __syncthreads();
+        if (threadIdx.x == 0) sh.n_list = 0;
+        __syncthreads();
+        const int n_spans = row.spans();
+        for (int s = 0; s < n_spans; s++) {
+            const int span = (row.span_at + (s ? 1 : 0)) % n_spans;  // the one in the registers first
+            if (s) row.load(span, sh.lut, [] {});
+            if (all || q.pos) row.collect(all ? q.pos : q.pos - 1, list, kListRoom, sh);
+        }
+        if (all) {
+            n = q.above + q.count;
+        } else {
+            n = min(q.above + q.count, (uint32_t)a.k);
+            row.first_of(q.pos, n - q.above, list + q.above, sh);
+        }
+    } else if (threadIdx.x == 0) {
+        a.lse[r] = -INFINITY;
+    }
+    __syncthreads();
+    write_top(list, n, a, r, [](uint32_t pos) { return bits_value(pos_bits(pos)); });
+}
+
+void launch_counts(const TopArgs &a, int batch, hipStream_t st) {
+    const int pieces = (a.V + 7 + kPieceIds - 1) / kPieceIds;  // 7: the largest skew
+    if (pieces <= 4) hipLaunchKernelGGL((k_top_counts<4>), dim3(batch), dim3(kRowThreads), 0, st, a);
+    else if (pieces <= 8) hipLaunchKernelGGL((k_top_counts<8>), dim3(batch), dim3(kRowThreads), 0, st, a);
+    else hipLaunchKernelGGL((k_top_counts<kMaxPieces>), dim3(batch), dim3(kRowThreads), 0, st, a);
+}
+
 }  // namespace
 
 }  // namespace cg
@@ -125,7 +214,7 @@ int cg_top_logits(const void *d_logits, int32_t dtype, int32_t batch, int32_t vo
     if (dtype == 0)
         hipLaunchKernelGGL((k_top_logits<0>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
     else
-        hipLaunchKernelGGL((k_top_logits<1>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
+        launch_counts(a, batch, (hipStream_t)stream);
     return launch_status("top_logits");
 }
 
