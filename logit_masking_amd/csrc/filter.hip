@@ -118,13 +118,73 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_sample(FilterArgs a) {
     }
 }
 
+// The place of the draw at u among what the filters keep, the pick being the
+// n-th candidate there, and the kept mass.
+template <int NP, bool SPANS>
+__device__ __forceinline__ HistPlace draw(HistOrder<NP, SPANS> &order, int k, float p, float mp, float u, double &mass,
+                                          uint32_t &n) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t top = order.top_pos();
+    uint32_t cut = 0xFFFFFFFFu, ties = 0;  // the last kept position, and how many of it stay
+    if (k > 0 && (uint32_t)k < order.total_count()) {
+        const HistPlace q = order.template find<0>((uint32_t)k - 1, 0.0);
+        cut = q.pos;
+        ties = (uint32_t)k - q.above;
+        mass = q.mass_above + ties * q.w;
+    }
+    if (p <= 0.f) {
+        cut = top;
+        ties = 1;
+        mass = 1.0;
+    } else if (p < 1.f) {
+        // rank j stays while the mass before it is under p * mass: the last
+        // one kept is the first whose own end reaches it
+        const double goal = (double)p * mass;
+        const HistPlace q = order.template find<2>(0, goal);
+        const uint32_t keep = min(q.count, (uint32_t)fmin(fmax(ceil((goal - q.mass_above) / q.w), 1.0), 4294967040.0));
+        if (q.pos < cut || (q.pos == cut && keep < ties)) {
+            cut = q.pos;
+            ties = keep;
+            mass = q.mass_above + ties * q.w;
+        }
+    }
+    if (mp > 0.f) {
+        // the last position whose weight reaches min_p (weights fall with the
+        // position): 64 points of the range at a time
+        const double least = fmin((double)mp, 1.0);
+        uint32_t lo = top, hi = 32768u + (uint32_t)kInfIdx;  // holds at lo, not at hi (-inf)
+        while (hi - lo > 1) {
+            const uint32_t step = (hi - lo + 63) / 64, at = min(lo + (uint32_t)lane * step, hi);
+            const uint64_t ok = __ballot(at < hi && order.weight(bits_value(pos_bits(at))) >= least);
+            const int l = 63 - __builtin_clzll(ok);  // lane 0 holds
+            lo = lo + (uint32_t)l * step;
+            hi = min(lo + step, hi);
+        }
+        if (lo < cut) {
+            cut = lo;
+            ties = 0xFFFFFFFFu;
+            mass = order.mass_to(lo);
+        }
+    }
+    const double at = u > 0.f ? fmin((double)u, 1.0 - 0x1p-53) * mass : 0.0;
+    HistPlace q = order.template find<1>(0, at);
+    uint32_t left = q.count;
+    if (q.pos >= cut) {
+        if (q.pos > cut) q = order.template find<1>(0, mass * (1.0 - 0x1p-50));
+        left = min(q.count, ties);
+    }
+    const double j = floor((at - q.mass_above) / q.w);
+    n = j > 0.0 ? min((uint32_t)fmin(j, 4294967040.0), left - 1) : 0u;
+    return q;
+}
+
 // bfloat16 rows: one read, the filters on the counts of the row's values
 // (row_hist.hpp).
-template <int NP>
+template <int NP, bool SPANS>
 __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     __shared__ HistShared sh;
-    const int r = blockIdx.x, lane = threadIdx.x & 63;
-    HistRow<NP> row;
+    const int r = blockIdx.x;
+    HistRow<NP, SPANS> row;
     row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
              a.wpr, a.V);
     const float T = a.temp[r];
@@ -133,7 +193,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     const float mp = a.min_p ? a.min_p[r] : 0.f;
     const float u = a.uniform[r];
     const bool greedy = !(T > 0.f);
-    HistOrder<NP> order(sh, row);
+    HistOrder<NP, SPANS> order(sh, row);
     if (!order.build(greedy ? 1.0 : 1.0 / (double)T)) {
         if (threadIdx.x == 0) {
             a.ids[r] = -1;
@@ -141,68 +201,19 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
         }
         return;
     }
-    const uint32_t top = order.top_pos();
-    double mass = order.total_mass();
-    uint32_t pos = top, n = 0, count;
-    if (greedy) {
-        count = order.template find<0>(0, 0.0).count;
-    } else {
-        uint32_t cut = 0xFFFFFFFFu, ties = 0;  // the last kept position, and how many of it stay
-        if (k > 0 && (uint32_t)k < order.total_count()) {
-            const HistPlace q = order.template find<0>((uint32_t)k - 1, 0.0);
-            cut = q.pos;
-            ties = (uint32_t)k - q.above;
-            mass = q.mass_above + ties * q.w;
+    if (order.searches()) {
+        double mass = order.total_mass();
+        uint32_t n = 0;
+        const HistPlace q = greedy ? order.template find<0>(0, 0.0) : draw(order, k, p, mp, u, mass, n);
+        if (threadIdx.x == 0) {
+            sh.place = q;
+            sh.n = n;
+            sh.mass = mass;
         }
-        if (p < 1.f) {
-            // rank j stays while the mass before it is under p * mass: the
-            // last one kept is the first whose own end reaches it
-            if (p <= 0.f) {
-                cut = top;
-                ties = 1;
-                mass = 1.0;
-            } else {
-                const double goal = (double)p * mass;
-                const HistPlace q = order.template find<2>(0, goal);
-                const uint32_t keep =
-                    min(q.count, (uint32_t)fmin(fmax(ceil((goal - q.mass_above) / q.w), 1.0), 4294967040.0));
-                if (q.pos < cut || (q.pos == cut && keep < ties)) {
-                    cut = q.pos;
-                    ties = keep;
-                    mass = q.mass_above + ties * q.w;
-                }
-            }
-        }
-        if (mp > 0.f) {
-            // the last position whose weight reaches min_p (weights fall with
-            // the position): 64 points of the range at a time
-            const double least = fmin((double)mp, 1.0);
-            uint32_t lo = top, hi = 32768u + (uint32_t)kInfIdx;  // holds at lo, not at hi (-inf)
-            while (hi - lo > 1) {
-                const uint32_t step = (hi - lo + 63) / 64, at = min(lo + (uint32_t)lane * step, hi);
-                const uint64_t ok = __ballot(at < hi && order.weight(bits_value(pos_bits(at))) >= least);
-                const int l = 63 - __builtin_clzll(ok);  // lane 0 holds
-                lo = lo + (uint32_t)l * step;
-                hi = min(lo + step, hi);
-            }
-            if (lo < cut) {
-                cut = lo;
-                ties = 0xFFFFFFFFu;
-                mass = order.mass_to(lo);
-            }
-        }
-        const double at = u > 0.f ? fmin((double)u, 1.0 - 0x1p-53) * mass : 0.0;
-        HistPlace q = order.template find<1>(0, at);
-        uint32_t left = q.count;
-        if (q.pos >= cut) {
-            if (q.pos > cut) q = order.template find<1>(0, mass * (1.0 - 0x1p-50));
-            left = min(q.count, ties);
-        }
-        pos = q.pos;
-        count = q.count;
-        const double j = floor((at - q.mass_above) / q.w);
-        n = j > 0.0 ? min((uint32_t)fmin(j, 4294967040.0), left - 1) : 0u;
     }
+    __syncthreads();
+    const uint32_t pos = sh.place.pos, count = sh.place.count, n = sh.n;
+    const double mass = sh.mass;
     const int id = row.nth(pos, count, n, sh);
     if (threadIdx.x == 0) {
         const double x = (double)bits_value(pos_bits(pos));
@@ -210,16 +221,6 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
         a.ids[r] = id;
         a.logprob[r] = (float)(y - log(mass));
     }
-}
-
-// Pieces of 8 ids a thread holds (row_hist.hpp): as many as the row needs, up
-// to 128 registers' worth beside what the kernel works with; longer rows are
-// taken in spans.
-void launch_counts(const FilterArgs &a, int batch, hipStream_t st) {
-    const int pieces = (a.V + 7 + kPieceIds - 1) / kPieceIds;  // 7: the largest skew
-    if (pieces <= 4) hipLaunchKernelGGL((k_filter_counts<4>), dim3(batch), dim3(kRowThreads), 0, st, a);
-    else if (pieces <= 8) hipLaunchKernelGGL((k_filter_counts<8>), dim3(batch), dim3(kRowThreads), 0, st, a);
-    else hipLaunchKernelGGL((k_filter_counts<kMaxPieces>), dim3(batch), dim3(kRowThreads), 0, st, a);
 }
 
 }  // namespace
@@ -258,7 +259,7 @@ int cg_filter_sample(const void *d_logits, int32_t dtype, int32_t batch, int32_t
     if (dtype == 0) {
         hipLaunchKernelGGL((k_filter_sample<0>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
     } else {
-        launch_counts(a, batch, (hipStream_t)stream);
+        CG_LAUNCH_ROWS(k_filter_counts, vocab, batch, (hipStream_t)stream, a);
     }
     return launch_status("filter_sample");
 }

@@ -18,31 +18,41 @@
 // Order positions run from the largest value down: position p < 32768 is the
 // value of bits 32767 - p, the others the negatives, magnitude rising.  The
 // two zeros (positions 32767 and 32768) are one value, kept at 32767.  A
-// block is 64 positions in a row, one per lane.
+// block is 256 positions in a row, four per lane.
 #pragma once
 #include "row_select.hpp"
 
 namespace cg {
 
-constexpr int kHistDwords = 32768;
+constexpr int kHistDwords = 32768, kHistBlocks = 256;
 constexpr int kPieceIds = 8 * kRowThreads;  // ids of one 16-byte load of every thread
-constexpr int kMaxPieces = 16;              // pieces a thread holds at most; shorter rows are launched with enough
 constexpr int kNegInfPair = (int)0xFF80FF80;
 constexpr int kInfIdx = 0x7F80;             // bits of +inf; larger ones are NaN
 constexpr int kBufWord3 = 0x00020000;       // raw buffer, 32-bit data format
+
+// A place in the order: the position, its candidates, those before it, their mass.
+struct HistPlace {
+    uint32_t pos, count, above;
+    double mass_above, w;
+};
 
 struct HistShared {
     uint32_t h[kHistDwords];
     uint32_t dummy[64];  // where lanes count what is no candidate
     uint4 lut[256];      // mask byte -> half of ones per allowed id of four pairs
-    uint32_t blk_cnt[1024];
-    double blk_mass[1024];
-    uint32_t w_cnt[kRowWaves];
-    double w_mass[kRowWaves];
+    uint32_t blk_cnt[kHistBlocks];
+    double blk_mass[kHistBlocks];
     uint32_t counted;    // sum of every count, the dummies' included
-    uint32_t top_pos;    // smallest order position with a candidate
+    uint32_t top_block;  // first block with a candidate
+    uint32_t n_blocks;   // blocks with a candidate, listed in any order
+    uint16_t blocks[kHistBlocks];
+    uint32_t list[kRowThreads];
     uint32_t n_list;
+    uint32_t w_cnt[kRowWaves];
     int found;
+    HistPlace place;     // what the searching wave found
+    uint32_t n;
+    double mass;
 };
 
 // ---- 64-lane inclusive scan (DPP: rows of 16, then row broadcasts) ----------
@@ -83,17 +93,11 @@ __device__ __forceinline__ uint32_t pos_bits(uint32_t pos) {
 }
 __device__ __forceinline__ float bits_value(uint32_t b) { return __uint_as_float(b << 16); }
 
-// A place in the order: the position, its candidates, those before it, their mass.
-struct HistPlace {
-    uint32_t pos, count, above;
-    double mass_above, w;
-};
-
-// The row: NP pieces a thread held in registers; rows longer than NP pieces
-// are taken in spans of NP.  Every load is 16 bytes from a 16-byte boundary:
+// The row: NP pieces a thread held in registers; with SPANS, longer rows are
+// taken in spans of NP.  Every load is 16 bytes from a 16-byte boundary:
 // a row that starts past one by `skew` ids is taken from the boundary, the
 // ids before its own start never allowed.
-template <int NP>
+template <int NP, bool SPANS>
 struct HistRow {
     static constexpr int kSpan = NP * kPieceIds;
     __amdgpu_buffer_rsrc_t rx, rm;
@@ -101,7 +105,8 @@ struct HistRow {
     const uint64_t *mask;
     int V, skew;
     uint32_t d[NP][4];
-    int span_at;  // the span in the registers
+    int span_at;    // the span in the registers
+    uint32_t live;  // bit p: the wave's piece p has an allowed id
 
     __device__ void init(const void *logits, const uint64_t *m, int wpr, int vocab) {
         x = (const uint16_t *)logits;
@@ -111,7 +116,7 @@ struct HistRow {
         rx = __builtin_amdgcn_make_buffer_rsrc((void *)(x - skew), (short)0, ((V + skew) * 2 + 3) & ~3, kBufWord3);
         rm = __builtin_amdgcn_make_buffer_rsrc((void *)m, (short)0, m ? (vocab + 63) / 64 * 8 : 0, kBufWord3);
     }
-    __device__ int spans() const { return NP < kMaxPieces ? 1 : (V + skew + kSpan - 1) / kSpan; }
+    __device__ int spans() const { return SPANS ? (V + skew + kSpan - 1) / kSpan : 1; }
     __device__ int first_id(int span, int p) const {
         return span * kSpan + p * kPieceIds + (int)threadIdx.x * 8 - skew;
     }
@@ -123,60 +128,121 @@ struct HistRow {
         return left >= 8 ? byte : left <= 0 ? 0u : byte & ((1u << left) - 1u);
     }
 
-    // Reads a span, what is not allowed as -inf.  The mask's bytes come first:
-    // a lane whose 8 ids are all masked asks past the buffer's end, which
-    // reads nothing (a constrained row's mask is mostly zeros).  while_waiting
-    // runs once the mask's loads are in flight.
-    template <class F>
-    __device__ __forceinline__ void load(int span, const uint4 *lut, F while_waiting) {
-        span_at = span;
-        const int base = span * kSpan;
-        uint32_t mb[NP];
+    // The mask bytes of a span's pieces as they lie (8 bits, or 16 that hold a skewed row's 8).
+    __device__ __forceinline__ void ask_mask(int span, uint32_t (&raw)[NP]) const {
 #pragma unroll
         for (int p = 0; p < NP; p++) {
-            mb[p] = 0xFFu;
+            raw[p] = 0xFFFFu;
             if (mask) {
-                const int q = (base + p * kPieceIds) / 8 + (int)threadIdx.x;
-                mb[p] = __builtin_amdgcn_raw_buffer_load_b8(rm, q, 0, 0);
-                if (skew) mb[p] = (mb[p] << 8) | __builtin_amdgcn_raw_buffer_load_b8(rm, q - 1, 0, 0);
-            }
-        }
-        while_waiting();
-#pragma unroll
-        for (int p = 0; p < NP; p++) {
-            const int first = first_id(span, p);
-            mb[p] = allowed8(mask && skew ? (mb[p] >> (8 - skew)) & 0xFFu : mb[p], first);
-            const uint4 v = __builtin_bit_cast(
-                uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, mb[p] ? (first + skew) * 2 : 0x7FFFFFF0, 0, 0));
-            d[p][0] = v.x; d[p][1] = v.y; d[p][2] = v.z; d[p][3] = v.w;
-        }
-#pragma unroll
-        for (int p = 0; p < NP; p++) {
-            if (mask || skew || base + (p + 1) * kPieceIds > V) {  // uniform
-                const uint4 s = lut[mb[p]];
-                d[p][0] = (d[p][0] & s.x) | (~s.x & kNegInfPair);
-                d[p][1] = (d[p][1] & s.y) | (~s.y & kNegInfPair);
-                d[p][2] = (d[p][2] & s.z) | (~s.z & kNegInfPair);
-                d[p][3] = (d[p][3] & s.w) | (~s.w & kNegInfPair);
+                const int q = (span * kSpan + p * kPieceIds) / 8 + (int)threadIdx.x;
+                raw[p] = __builtin_amdgcn_raw_buffer_load_b8(rm, q, 0, 0);
+                if (skew) raw[p] = (raw[p] << 8) | __builtin_amdgcn_raw_buffer_load_b8(rm, q - 1, 0, 0);
             }
         }
     }
+    __device__ __forceinline__ uint32_t usable(int span, int p, uint32_t raw) const {
+        return allowed8(skew ? (raw >> (8 - skew)) & 0xFFu : raw & 0xFFu, first_id(span, p));
+    }
+    // Asks for a piece.  A lane whose 8 ids are all masked asks past the
+    // buffer's end, which reads nothing (a constrained row's mask is mostly
+    // zeros); without a branch, so that the loads stay in flight together.
+    __device__ __forceinline__ void ask(int span, int p, bool any) {
+        const uint4 v = __builtin_bit_cast(
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, any ? (first_id(span, p) + skew) * 2 : 0x7FFFFFF0, 0, 0));
+        d[p][0] = v.x; d[p][1] = v.y; d[p][2] = v.z; d[p][3] = v.w;
+    }
+    // Piece p's ids that are not allowed become -inf (bytes: piece p's in
+    // byte p % 4 of word p / 4).
+    static constexpr int kWords = (NP + 3) / 4;
+    __device__ __forceinline__ void select(int span, int p, const uint32_t (&bytes)[kWords], const uint4 *lut) {
+        if (mask || skew || span * kSpan + (p + 1) * kPieceIds > V) {  // uniform
+            const uint4 s = lut[(bytes[p / 4] >> (8 * (p % 4))) & 0xFFu];
+            d[p][0] = (d[p][0] & s.x) | (~s.x & kNegInfPair);
+            d[p][1] = (d[p][1] & s.y) | (~s.y & kNegInfPair);
+            d[p][2] = (d[p][2] & s.z) | (~s.z & kNegInfPair);
+            d[p][3] = (d[p][3] & s.w) | (~s.w & kNegInfPair);
+        }
+    }
+    static __device__ __forceinline__ uint32_t bit_if_any(bool v, int p) { return (__ballot(v) ? 1u : 0u) << p; }
 
-    // Counts the registers' values.  -inf and negative NaNs go to the lane's
-    // own dummy (a run of one value would queue at one address).
-    __device__ __forceinline__ void count(HistShared &sh) {
+    // Asks for the pieces from `from` on and notes which may be used.
+    __device__ __forceinline__ void ask_rest(int span, int from, const uint32_t (&raw)[NP], uint32_t (&bytes)[kWords]) {
+        live = 0;
+#pragma unroll
+        for (int p = 0; p < NP; p++) {
+            const uint32_t b = usable(span, p, raw[p]);
+            bytes[p / 4] = (p % 4 ? bytes[p / 4] : 0u) | b << (8 * (p % 4));
+            live |= bit_if_any(b != 0, p);
+            if (p >= from) ask(span, p, b != 0);
+        }
+    }
+
+    // Reads a span.
+    __device__ __forceinline__ void load(int span, const uint4 *lut) {
+        uint32_t raw[NP], bytes[kWords];
+        span_at = span;
+        ask_mask(span, raw);
+        ask_rest(span, 0, raw, bytes);
+#pragma unroll
+        for (int p = 0; p < NP; p++)
+            if ((live >> p) & 1) select(span, p, bytes, lut);
+    }
+
+    // Reads and counts the whole row.  The first quarter of the first span is
+    // asked for before the mask is known, so that memory is busy meanwhile;
+    // while_waiting runs then.  Of a longer row each piece is asked for as soon
+    // as the one before it in its registers is counted.  The last span stays
+    // in the registers.
+    template <class F>
+    __device__ __forceinline__ void read_and_count(HistShared &sh, F while_waiting) {
+        constexpr int kEager = NP / 4;
+        uint32_t raw[NP], bytes[kWords], dead = 0;
+        const int n_spans = spans();
+        ask_mask(0, raw);
+#pragma unroll
+        for (int p = 0; p < kEager; p++) ask(0, p, true);
+        while_waiting();
+        ask_rest(0, kEager, raw, bytes);
+        __syncthreads();  // the counts are cleared
+        for (span_at = 0;; span_at++) {
+            const bool more = span_at + 1 < n_spans;  // uniform
+            uint32_t live_next = 0, bytes_next[kWords];
+            if (more) ask_mask(span_at + 1, raw);
+#pragma unroll
+            for (int p = 0; p < NP; p++) {
+                if ((live >> p) & 1) {
+                    select(span_at, p, bytes, sh.lut);
+                    count(p, sh);
+                } else {
+                    dead++;
+                }
+                if (more) {
+                    const uint32_t b = usable(span_at + 1, p, raw[p]);
+                    bytes_next[p / 4] = (p % 4 ? bytes_next[p / 4] : 0u) | b << (8 * (p % 4));
+                    live_next |= bit_if_any(b != 0, p);
+                    ask(span_at + 1, p, b != 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (!more) break;
+            live = live_next;
+#pragma unroll
+            for (int i = 0; i < kWords; i++) bytes[i] = bytes_next[i];
+        }
+        if ((threadIdx.x & 63) == 0 && dead) atomicAdd(&sh.counted, dead * 512u);  // of one wave
+    }
+
+    // Counts a piece.  -inf and negative NaNs go to the lane's own dummy (a
+    // run of one value would queue at one address).
+    __device__ __forceinline__ void count(int p, HistShared &sh) {
         char *h = (char *)sh.h;
         const uint32_t none = (uint32_t)((char *)&sh.dummy[threadIdx.x & 63] - h);
 #pragma unroll
-        for (int p = 0; p < NP; p++) {
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const uint32_t w = d[p][j];
-                const uint32_t a0 = (w << 2) & 0x1FFFCu, a1 = (w >> 14) & 0x1FFFCu;
-                atomicAdd((uint32_t *)(h + ((uint16_t)w < 0xFF80u ? a0 : none)), (w & 0x8000u) ? 0x10000u : 1u);
-                atomicAdd((uint32_t *)(h + (w < 0xFF800000u ? a1 : none)), (int)w < 0 ? 0x10000u : 1u);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < 4; j++) {
+            const uint32_t w = d[p][j];
+            const uint32_t a0 = (w << 2) & 0x1FFFCu, a1 = (w >> 14) & 0x1FFFCu;
+            atomicAdd((uint32_t *)(h + ((uint16_t)w < 0xFF80u ? a0 : none)), (w & 0x8000u) ? 0x10000u : 1u);
+            atomicAdd((uint32_t *)(h + (w < 0xFF800000u ? a1 : none)), (int)w < 0 ? 0x10000u : 1u);
         }
     }
 
@@ -193,6 +259,7 @@ struct HistRow {
         const uint32_t b = last == 32767u ? 0x8000u : pos_bits(last);
 #pragma unroll
         for (int p = 0; p < NP; p++) {
+            if (!((live >> p) & 1)) continue;
             bool hit;
             if (pos) {  // uniform
                 s16x2 m = __builtin_elementwise_max(__builtin_bit_cast(s16x2, d[p][0]), __builtin_bit_cast(s16x2, d[p][1]));
@@ -254,108 +321,275 @@ struct HistRow {
         walk(pos, upto, sh, [&](uint32_t rank, int id) { list[rank] = ((uint64_t)pos << 32) | (uint32_t)id; });
     }
 
+    // Lists the ids of the registers' candidates of one value, any order.
+    __device__ __forceinline__ void matches(uint32_t want, uint32_t same, uint32_t *list, HistShared &sh) {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int p = 0; p < NP; p++) {
+            if (!((live >> p) & 1)) continue;
+            const uint32_t y0 = (d[p][0] ^ want) & same, y1 = (d[p][1] ^ want) & same;
+            const uint32_t y2 = (d[p][2] ^ want) & same, y3 = (d[p][3] ^ want) & same;
+            u16x2 m = __builtin_elementwise_min(__builtin_bit_cast(u16x2, y0), __builtin_bit_cast(u16x2, y1));
+            m = __builtin_elementwise_min(
+                m, __builtin_elementwise_min(__builtin_bit_cast(u16x2, y2), __builtin_bit_cast(u16x2, y3)));
+            if (m.x == 0 || m.y == 0) {
+                uint32_t at = ((y0 & 0xFFFFu) ? 0u : 1u) | ((y0 >> 16) ? 0u : 2u) | ((y1 & 0xFFFFu) ? 0u : 4u) |
+                              ((y1 >> 16) ? 0u : 8u) | ((y2 & 0xFFFFu) ? 0u : 16u) | ((y2 >> 16) ? 0u : 32u) |
+                              ((y3 & 0xFFFFu) ? 0u : 64u) | ((y3 >> 16) ? 0u : 128u);
+                do {  // nearly always one
+                    list[atomicAdd(&sh.n_list, 1u)] = first_id(span_at, p) + __builtin_ctz(at);
+                    at &= at - 1;
+                } while (at);
+            }
+        }
+    }
+
     // The id of the n-th (from 0) of the row's `count` candidates of position
     // pos, by rising id.
     __device__ int nth(uint32_t pos, uint32_t count, uint32_t n, HistShared &sh) {
         const uint32_t bits = pos_bits(pos);
         const uint32_t same = bits == 0 ? 0x7FFF7FFFu : 0xFFFFFFFFu;  // the two zeros
         const uint32_t want = bits | (bits << 16);
-        uint32_t *list = sh.blk_cnt;  // no longer needed
-        // match bits of a piece
-        auto match = [&](int p) -> uint32_t {
-            uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const uint32_t y = (d[p][j] ^ want) & same;
-                m |= ((y & 0xFFFFu) == 0 ? 1u : 0u) << (2 * j);
-                m |= ((y >> 16) == 0 ? 1u : 0u) << (2 * j + 1);
-            }
-            return m;
-        };
-        if (count <= 512) {
-            // few: list their ids in any order, the n-th is the one with n smaller ones
-            __syncthreads();
-            if (threadIdx.x == 0) sh.n_list = 0;
-            __syncthreads();
-            const int n_spans = spans();
-            for (int s = 0; s < n_spans; s++) {
-                const int span = (span_at + (s ? 1 : 0)) % n_spans;  // the one in the registers first
-                if (s) load(span, sh.lut, [] {});
-#pragma unroll
-                for (int p = 0; p < NP; p++) {
-                    uint32_t m = match(p);
-                    while (m) {
-                        const int j = __builtin_ctz(m);
-                        m &= m - 1;
-                        list[atomicAdd(&sh.n_list, 1u)] = first_id(span, p) + j;
-                    }
-                }
-                __syncthreads();
-                if (sh.n_list >= count) break;  // uniform
-            }
-            if (threadIdx.x < count) {
-                const uint32_t id = list[threadIdx.x];
-                uint32_t smaller = 0;
-                for (uint32_t i = 0; i < count; i++) smaller += list[i] < id;
-                if (smaller == n) sh.found = (int)id;
-            }
-            __syncthreads();
+        uint32_t *list = sh.list;
+        if (count > kRowThreads) {
+            // many: walk the row again
+            if (threadIdx.x == 0) sh.found = -1;
+            walk(pos, n + 1, sh, [&](uint32_t rank, int id) {
+                if (rank == n) sh.found = id;
+            });
             return sh.found;
         }
-        // many: walk the row again
-        if (threadIdx.x == 0) sh.found = -1;
-        walk(pos, n + 1, sh, [&](uint32_t rank, int id) {
-            if (rank == n) sh.found = id;
-        });
+        // few: list them; the n-th is the one with n smaller ones.  A longer
+        // row's last span is in the registers: its ids are the largest, the
+        // other spans are read again only if the n-th is not among them.
+        auto clear = [&] {
+            __syncthreads();
+            if (threadIdx.x == 0) sh.n_list = 0;
+            list[threadIdx.x] = 0xFFFFFFFFu;
+            __syncthreads();
+        };
+        clear();
+        matches(want, same, list, sh);
+        __syncthreads();
+        uint32_t listed = sh.n_list;
+        const int n_spans = spans();
+        if (n_spans > 1) {
+            const uint32_t before = count - listed;
+            if (n >= before) {
+                n -= before;
+            } else {
+                clear();
+                listed = 0;
+                for (int s = 0; s + 1 < n_spans && listed <= n; s++) {  // uniform
+                    load(s, sh.lut);
+                    matches(want, same, list, sh);
+                    __syncthreads();
+                    listed = sh.n_list;
+                    __syncthreads();
+                }
+            }
+        }
+        if (threadIdx.x < listed) {
+            const uint32_t id = list[threadIdx.x];
+            const uint4 *four = (const uint4 *)list;
+            uint32_t smaller = 0;
+#pragma unroll 4
+            for (uint32_t i = 0; i < (listed + 3) / 4; i++) {
+                const uint4 v = four[i];
+                smaller += (v.x < id) + (v.y < id) + (v.z < id) + (v.w < id);
+            }
+            if (smaller == n) sh.found = (int)id;
+        }
+        __syncthreads();
         return sh.found;
     }
 };
 
-// The counted row: totals by block, and the searches.  Every wave runs the
-// searches alike, so no result is handed over.
-template <int NP>
-struct HistOrder {
-    HistShared &sh;
-    HistRow<NP> &row;
-    Weight weight;
-    int wide;  // -1: h holds both signs in 16 bits; 0 / 1: that sign in 32 bits
-    // lane w < 16: candidates and mass before, and up to the end of, the 64 blocks of w
-    uint32_t w_above, w_incl;
-    double w_mass_above, w_mass_incl;
+// sum + the two 16-bit halves of c
+__device__ __forceinline__ uint32_t add_halves(uint32_t c, uint32_t sum) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_udot2(__builtin_bit_cast(u16x2, c), (u16x2){1, 1}, sum, false);
+}
 
-    __device__ __forceinline__ HistOrder(HistShared &s, HistRow<NP> &r) : sh(s), row(r) {}
-
-    static __device__ __forceinline__ void clear(HistShared &sh) {
-        uint4 *h = (uint4 *)sh.h;
+__device__ __forceinline__ void clear_counts(HistShared &sh) {
+    uint4 *h = (uint4 *)sh.h;
 #pragma unroll
-        for (int i = 0; i < kHistDwords / 4 / kRowThreads; i++) h[threadIdx.x + i * kRowThreads] = make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < kHistDwords / 4 / kRowThreads; i++) h[threadIdx.x + i * kRowThreads] = make_uint4(0, 0, 0, 0);
+}
 
-    // Counts of dword i, cleaned: no NaN, both zeros in the positive one.
-    __device__ __forceinline__ void cleaned(int i, uint32_t c, uint32_t &pos, uint32_t &neg) const {
-        pos = wide < 0 ? c & 0xFFFFu : wide == 0 ? c : 0u;
-        neg = wide < 0 ? c >> 16 : wide == 1 ? c : 0u;
-        if (i > kInfIdx) pos = 0;
-        if (i == 0) {
-            pos += neg;
-            neg = 0;
+// What dword i counts, without NaN, both zeros as the positive one.  wide: -1:
+// both signs in 16 bits, 0 / 1: that sign in 32.
+__device__ __forceinline__ void cleaned(int wide, int i, uint32_t c, uint32_t &pos, uint32_t &neg) {
+    pos = wide < 0 ? c & 0xFFFFu : wide == 0 ? c : 0u;
+    neg = wide < 0 ? c >> 16 : wide == 1 ? c : 0u;
+    if (i > kInfIdx) pos = 0;
+    if (i == 0) {
+        pos += neg;
+        neg = 0;
+    }
+}
+// Candidates of the lane's four order positions of a block, b * 256 + 4 lane + j.
+__device__ __forceinline__ void bins(const HistShared &sh, int wide, int b, uint32_t (&c)[4]) {
+    const int lane = threadIdx.x & 63;
+    const bool neg = b >= kHistBlocks / 2;  // uniform
+    const int q = neg ? (b - kHistBlocks / 2) * 64 + lane : (kHistBlocks / 2 - 1 - b) * 64 + 63 - lane;
+    const uint4 v = ((const uint4 *)sh.h)[q];
+    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        uint32_t cp, cn;
+        const int at = neg ? j : 3 - j;
+        cleaned(wide, q * 4 + at, neg ? d[j] : d[3 - j], cp, cn);
+        c[j] = neg ? cn : cp;
+    }
+}
+// Weights of those positions; 1 where there is no candidate (a value above
+// the largest one may weigh inf).
+__device__ __forceinline__ void bin_weights(const Weight &weight, int b, const uint32_t (&c)[4], double (&w)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        w[j] = weight(c[j] ? bits_value(pos_bits(b * 256 + 4 * (threadIdx.x & 63) + j)) : (float)weight.m);
+}
+
+// Lists the blocks that hold candidates and notes the first; where asked,
+// sums all counts.  A wave takes 256 dwords at a time, 4 a lane: a block of
+// positives and one of negatives.
+__device__ __forceinline__ void survey(HistShared &sh, int wide, bool sum_up) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint4 *h4 = (const uint4 *)sh.h;
+    uint32_t sum = 0;
+#pragma unroll
+    for (int part = 0; part < 4; part++) {
+        uint4 c[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) c[i] = h4[(wave + 16 * (2 * part + i)) * 64 + lane];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int g = wave + 16 * (2 * part + i);
+            if (sum_up) {
+                sum = add_halves(c[i].x, add_halves(c[i].y, sum));
+                sum = add_halves(c[i].z, add_halves(c[i].w, sum));
+            }
+            const uint32_t all = c[i].x | c[i].y | c[i].z | c[i].w;
+            uint32_t pos = wide < 0 ? all & 0xFFFFu : wide == 0 ? all : 0u;
+            uint32_t neg = wide < 0 ? all >> 16 : wide == 1 ? all : 0u;
+            if (g == 0 || g == kHistDwords / 256 - 1) {  // zeros and NaNs
+                pos = neg = 0;
+                const uint32_t v[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    uint32_t cp, cn;
+                    cleaned(wide, g * 256 + lane * 4 + j, v[j], cp, cn);
+                    pos |= cp;
+                    neg |= cn;
+                }
+            }
+            const bool has_pos = __ballot(pos != 0) != 0, has_neg = __ballot(neg != 0) != 0;
+            if (lane < 2 && (lane ? has_neg : has_pos)) {
+                const int b = lane ? kHistBlocks / 2 + g : kHistBlocks / 2 - 1 - g;
+                sh.blocks[atomicAdd(&sh.n_blocks, 1u)] = (uint16_t)b;
+                atomicMin(&sh.top_block, (uint32_t)b);
+            }
         }
     }
-    // Candidates of order position b * 64 + lane.
-    __device__ __forceinline__ uint32_t bin(int b) const {
-        const int lane = threadIdx.x & 63;
-        const int i = b >= 512 ? (b - 512) * 64 + lane : (511 - b) * 64 + 63 - lane;
-        uint32_t pos, neg;
-        cleaned(i, sh.h[i], pos, neg);
-        return b >= 512 ? neg : pos;
+    if (sum_up) {
+        if (wave == 0) sum = add_halves(sh.dummy[lane], sum);
+        sum = (uint32_t)wave_scan((int)sum);
+        if (lane == 63) atomicAdd(&sh.counted, sum);
     }
+}
+
+// Totals of the listed blocks, a block a wave.
+__device__ __forceinline__ void total(HistShared &sh, int wide, const Weight &weight) {
+    const int wave = threadIdx.x >> 6, n = (int)sh.n_blocks;
+    for (int e = wave; e < n; e += kRowWaves) {
+        const int b = sh.blocks[e];
+        uint32_t c[4];
+        double w[4];
+        bins(sh, wide, b, c);
+        bin_weights(weight, b, c, w);
+        const double m = wave_scan(((double)c[0] * w[0] + (double)c[1] * w[1]) + ((double)c[2] * w[2] + (double)c[3] * w[3]));
+        const int s = wave_scan((int)(c[0] + c[1] + c[2] + c[3]));
+        if ((threadIdx.x & 63) == 63) {
+            sh.blk_cnt[b] = (uint32_t)s;
+            sh.blk_mass[b] = m;
+        }
+    }
+}
+
+// The largest candidate's position, from the first block.
+__device__ __forceinline__ uint32_t top_position(const HistShared &sh, int wide) {
+    const int b = (int)sh.top_block;
+    uint32_t c[4];
+    bins(sh, wide, b, c);
+    const int first = c[0] ? 0 : c[1] ? 1 : c[2] ? 2 : 3;
+    const int lane = __builtin_ctzll(__ballot((c[0] | c[1] | c[2] | c[3]) != 0));
+    return b * 256 + lane * 4 + lane_int(first, lane);
+}
+
+// Counts the candidates of one sign in 32 bits.
+__device__ __forceinline__ void recount(HistShared &sh, const uint16_t *x, const uint64_t *mask, int V, int sign) {
+    __syncthreads();
+    clear_counts(sh);
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < V; i += kRowThreads) {
+        if (mask && !((mask[i >> 6] >> (i & 63)) & 1)) continue;
+        const uint32_t v = x[i];
+        if (v >= 0xFF80u || (v > 0x8000u) != (sign != 0)) continue;
+        atomicAdd(&sh.h[v & 0x7FFFu], 1u);
+    }
+    __syncthreads();
+}
+// The totals of a row one of whose counts overflowed; the positives first, so
+// that the largest candidate is known before its weights are needed.  Returns
+// its position; the negatives' counts stay in h.
+__device__ __forceinline__ uint32_t total_wide(HistShared &sh, const uint16_t *x, const uint64_t *mask, int V, double inv_t) {
+    __syncthreads();
+    if (threadIdx.x == 0) sh.top_block = 0xFFFFFFFFu;
+    uint32_t top = 0xFFFFFFFFu;
+#pragma unroll 1
+    for (int sign = 0; sign < 2; sign++) {
+        recount(sh, x, mask, V, sign);
+        if (threadIdx.x == 0) sh.n_blocks = 0;
+        __syncthreads();
+        survey(sh, sign, false);
+        __syncthreads();
+        if (top == 0xFFFFFFFFu && sh.top_block != 0xFFFFFFFFu) top = top_position(sh, sign);
+        total(sh, sign, Weight{(double)bits_value(pos_bits(top)), inv_t});
+    }
+    return top;
+}
+
+// The counted row: totals by block, and the searches, which one wave runs
+// (a workgroup's worth of waves running them alike costs their instructions
+// sixteen times: 5 us of 35 at 256 rows of 128256).  Only in a row counted
+// one sign at a time do all waves run them, since a search may count again.
+template <int NP, bool SPANS>
+struct HistOrder {
+    HistShared &sh;
+    HistRow<NP, SPANS> &row;
+    Weight weight;
+    int wide;  // -1: h holds both signs in 16 bits; 0 / 1: that sign in 32 bits
+    // Candidates and mass up to the end of the lane's blocks 4 lane + j.
+    uint32_t incl;
+    double mass_incl;
+    __device__ __forceinline__ void blocks(uint32_t (&bc)[4], double (&bm)[4]) const {
+        const int lane = threadIdx.x & 63;
+        const uint4 c = ((const uint4 *)sh.blk_cnt)[lane];
+        bc[0] = c.x; bc[1] = c.y; bc[2] = c.z; bc[3] = c.w;
+#pragma unroll
+        for (int j = 0; j < 4; j++) bm[j] = sh.blk_mass[4 * lane + j];
+    }
+
+    __device__ __forceinline__ HistOrder(HistShared &s, HistRow<NP, SPANS> &r) : sh(s), row(r) {}
 
     // Reads, counts and orders the row under weights 1 / T.  False: no candidate.
     __device__ bool build(double inv_t) {
-        const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+        const int t = threadIdx.x;
         wide = -1;
-        row.load(0, sh.lut, [&] {
-            clear(sh);
+        row.read_and_count(sh, [&] {
+            clear_counts(sh);
             if (t < 64) sh.dummy[t] = 0;
             if (t < 256) {
                 uint32_t m[4];
@@ -364,193 +598,150 @@ struct HistOrder {
                     m[p] = ((t >> (2 * p)) & 1 ? 0x0000FFFFu : 0u) | ((t >> (2 * p + 1)) & 1 ? 0xFFFF0000u : 0u);
                 sh.lut[t] = make_uint4(m[0], m[1], m[2], m[3]);
             }
-            sh.blk_cnt[t] = 0;
-            sh.blk_mass[t] = 0.0;
+            if (t < kHistBlocks) {
+                sh.blk_cnt[t] = 0;
+                sh.blk_mass[t] = 0.0;
+            }
             if (t == 0) {
                 sh.counted = 0;
-                sh.top_pos = 0xFFFFFFFFu;
+                sh.n_blocks = 0;
+                sh.top_block = 0xFFFFFFFFu;
             }
-            __syncthreads();
         });
-        row.count(sh);
-        const int n_spans = row.spans();
-        for (int s = 1; s < n_spans; s++) {
-            row.load(s, sh.lut, [] {});
-            row.count(sh);
-        }
         __syncthreads();
-        uint32_t pg, ng;
-        survey(pg, ng, true);
+        const bool check = row.V > 65535;  // a count may have overflowed
+        survey(sh, -1, check);
         __syncthreads();
-        if (sh.counted != (uint32_t)n_spans * (uint32_t)HistRow<NP>::kSpan) {
-            // a count overflowed
-            if (t == 0) sh.top_pos = 0xFFFFFFFFu;
-            for (int sign = 0; sign < 2; sign++) {
-                recount(sign);
-                survey(pg, ng, false);
-                __syncthreads();
-                top_pos_ = sh.top_pos;
-                if (top_pos_ != 0xFFFFFFFFu) {
-                    weight = Weight{(double)bits_value(pos_bits(top_pos_)), inv_t};
-                    total(pg, ng);
-                }
-            }
-        } else {
-            top_pos_ = sh.top_pos;
+        if (check && sh.counted != (uint32_t)row.spans() * (uint32_t)HistRow<NP, SPANS>::kSpan) {
+            top_pos_ = total_wide(sh, row.x, row.mask, row.V, inv_t);
             if (top_pos_ == 0xFFFFFFFFu) return false;
+            wide = 1;
             weight = Weight{(double)bits_value(pos_bits(top_pos_)), inv_t};
-            total(pg, ng);
+        } else {
+            if (sh.top_block == 0xFFFFFFFFu) return false;
+            top_pos_ = top_position(sh, -1);
+            weight = Weight{(double)bits_value(pos_bits(top_pos_)), inv_t};
+            total(sh, -1, weight);
         }
         __syncthreads();
-        if (top_pos_ == 0xFFFFFFFFu) return false;
-        // inclusive sums over each wave's 64 blocks, then over the waves
-        const int b = wave * 64 + lane;
-        const uint32_t c = (uint32_t)wave_scan((int)sh.blk_cnt[b]);
-        const double m = wave_scan(sh.blk_mass[b]);
-        sh.blk_cnt[b] = c;
-        sh.blk_mass[b] = m;
-        if (lane == 63) {
-            sh.w_cnt[wave] = c;
-            sh.w_mass[wave] = m;
+        if (searches()) {
+            uint32_t bc[4];
+            double bm[4];
+            blocks(bc, bm);
+            incl = (uint32_t)wave_scan((int)(bc[0] + bc[1] + bc[2] + bc[3]));
+            mass_incl = wave_scan((bm[0] + bm[1]) + (bm[2] + bm[3]));
         }
-        __syncthreads();
-        const uint32_t wc = lane < kRowWaves ? sh.w_cnt[lane] : 0u;
-        const double wm = lane < kRowWaves ? sh.w_mass[lane] : 0.0;
-        w_incl = (uint32_t)wave_scan((int)wc);
-        w_mass_incl = wave_scan(wm);
-        w_above = w_incl - wc;
-        w_mass_above = from_left(w_mass_incl);
         return true;
     }
     // (These read other lanes: every lane calls them.)
+    __device__ bool searches() const { return wide >= 0 || threadIdx.x < 64; }
     __device__ uint32_t top_pos() const { return top_pos_; }
-    __device__ double total_mass() const { return lane_double(w_mass_incl, kRowWaves - 1); }
-    __device__ uint32_t total_count() const { return (uint32_t)lane_int((int)w_incl, kRowWaves - 1); }
+    __device__ double total_mass() const { return lane_double(mass_incl, 63); }
+    __device__ uint32_t total_count() const { return (uint32_t)lane_int((int)incl, 63); }
 
-    // The first position up to whose end there are more than `rank`
-    // candidates (HOW 0), more than `mass` (1), at least `mass` (2); the last
-    // one with a candidate (0) or with weight (1, 2) if there is none.
+    // Of four items a lane, in lane order: the first up to whose end there
+    // are more than `rank` candidates (HOW 0), more than `mass` (1), at least
+    // `mass` (2); the last one with a candidate (0) or with weight (1, 2) if
+    // there is none.  c, m: an item's own; ci, mi: the lane's inclusive sums;
+    // c0, m0: what lies before all.  Returns its number, the sums before it
+    // in c0, m0.
+    template <int HOW>
+    __device__ __forceinline__ int pick(const uint32_t (&c)[4], const double (&m)[4], uint32_t ci, double mi, uint32_t rank,
+                                        double mass, uint32_t &c0, double &m0) const {
+        auto reached = [&](uint32_t cs, double ms) { return HOW == 0 ? cs > rank : HOW == 1 ? ms > mass : ms >= mass; };
+        auto some = [&](uint32_t cs, double ms) { return HOW == 0 ? cs != 0 : ms > 0.0; };
+        const bool full = some(c[0] | c[1] | c[2] | c[3], (m[0] + m[1]) + (m[2] + m[3]));
+        const uint64_t f = __ballot(full), h = __ballot(full && reached(c0 + ci, m0 + mi));
+        const int L = h ? __builtin_ctzll(h) : f ? 63 - __builtin_clzll(f) : 0;
+        // every lane looks at its own four as if it were the one
+        uint32_t cb = c0 + ci - (c[0] + c[1] + c[2] + c[3]);
+        double mb = m0 + from_left(mi);
+        int at = 0;
+        bool done = false;
+        uint32_t c_at = cb;
+        double m_at = mb;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (!done && some(c[j], m[j])) {
+                at = j;
+                c_at = cb;
+                m_at = mb;
+                done = reached(cb + c[j], mb + m[j]);
+            }
+            cb += c[j];
+            mb += m[j];
+        }
+        c0 = (uint32_t)lane_int((int)c_at, L);
+        m0 = lane_double(m_at, L);
+        return 4 * L + lane_int(at, L);
+    }
+
+    // The place of the first position up to whose end ... (see pick).
     template <int HOW>
     __device__ HistPlace find(uint32_t rank, double mass) {
-        const int lane = threadIdx.x & 63;
-        auto reached = [&](uint32_t c, double m) { return HOW == 0 ? c > rank : HOW == 1 ? m > mass : m >= mass; };
-        auto some = [&](uint32_t c, double m) { return HOW == 0 ? c != 0 : m > 0.0; };
-        auto pick = [&](bool hit, bool full) {  // the first hit, else the last that is not empty
-            const uint64_t h = __ballot(hit && full), f = __ballot(full);
-            return h ? __builtin_ctzll(h) : f ? 63 - __builtin_clzll(f) : 0;
-        };
-        const int W = pick(reached(w_incl, w_mass_incl),
-                           lane < kRowWaves && some(w_incl - w_above, w_mass_incl - w_mass_above));
-        const uint32_t wc = (uint32_t)lane_int((int)w_above, W);
-        const double wm = lane_double(w_mass_above, W);
-        const uint32_t bc = sh.blk_cnt[W * 64 + lane];
-        const double bm = sh.blk_mass[W * 64 + lane];
-        const uint32_t bc0 = (uint32_t)from_left((int)bc);
-        const double bm0 = from_left(bm);
-        const int B = pick(reached(wc + bc, wm + bm), some(bc - bc0, bm - bm0));
-        const int b = W * 64 + B;
-        const uint32_t c_above = wc + (uint32_t)lane_int((int)bc0, B);
-        const double m_above = wm + lane_double(bm0, B);
-        hold(b);
-        const uint32_t c = bin(b);
-        const double w = c ? weight(bits_value(pos_bits(b * 64 + lane))) : 0.0;
-        const uint32_t ci = (uint32_t)wave_scan((int)c);
-        const double mi = wave_scan((double)c * w);
-        const int L = pick(reached(c_above + ci, m_above + mi), some(c, (double)c * w));
         HistPlace q;
-        q.pos = b * 64 + L;
-        q.count = (uint32_t)lane_int((int)c, L);
-        q.above = c_above + (uint32_t)lane_int((int)(ci - c), L);
-        q.mass_above = m_above + (L ? lane_double(mi, L - 1) : 0.0);
-        q.w = lane_double(w, L);
+        q.above = 0;
+        q.mass_above = 0.0;
+        uint32_t c[4];
+        double w[4], m[4];
+        blocks(c, m);
+        const int b = pick<HOW>(c, m, incl, mass_incl, rank, mass, q.above, q.mass_above);
+        hold(b);
+        bins(sh, wide, b, c);
+        bin_weights(weight, b, c, w);
+#pragma unroll
+        for (int j = 0; j < 4; j++) m[j] = (double)c[j] * w[j];
+        const uint32_t ci = (uint32_t)wave_scan((int)(c[0] + c[1] + c[2] + c[3]));
+        const double mi = wave_scan((m[0] + m[1]) + (m[2] + m[3]));
+        const int i = pick<HOW>(c, m, ci, mi, rank, mass, q.above, q.mass_above);
+        const int j = i & 3;
+        q.pos = b * 256 + i;
+        q.count = (uint32_t)lane_int((int)(j == 0 ? c[0] : j == 1 ? c[1] : j == 2 ? c[2] : c[3]), i >> 2);
+        q.w = lane_double(j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3], i >> 2);
         return q;
     }
 
     // Mass of the positions up to pos, its own included.
     __device__ double mass_to(uint32_t pos) {
-        const int b = pos >> 6, W = b >> 6, lane = threadIdx.x & 63;
-        const double above = lane_double(w_mass_above, W) + ((b & 63) ? sh.blk_mass[b - 1] : 0.0);
+        const int b = pos >> 8, lane = threadIdx.x & 63, at = (int)(pos & 255u);
+        double before = from_left(mass_incl), m = 0.0, w[4];
+        uint32_t c[4];
+        blocks(c, w);
+#pragma unroll
+        for (int j = 0; j < 3; j++) before += j < (b & 3) ? w[j] : 0.0;
+        before = lane_double(before, b >> 2);
         hold(b);
-        const uint32_t c = bin(b);
-        const double mi = wave_scan(c ? (double)c * weight(bits_value(pos_bits(b * 64 + lane))) : 0.0);
-        return above + lane_double(mi, pos & 63);
+        bins(sh, wide, b, c);
+        bin_weights(weight, b, c, w);
+#pragma unroll
+        for (int j = 0; j < 4; j++) m += 4 * lane + j <= at ? (double)c[j] * w[j] : 0.0;
+        return before + lane_double(wave_scan(m), 63);
     }
 
   private:
     uint32_t top_pos_;
 
-    // Which of the wave's 32 groups of 64 dwords (wave + 16 i) hold positive
-    // and negative candidates; the smallest position with one and, where
-    // asked, the sum of all counts go to LDS.
-    __device__ void survey(uint32_t &pg, uint32_t &ng, bool sum_up) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        uint32_t sum = 0, top = 0xFFFFFFFFu;
-        pg = ng = 0;
-#pragma unroll 8
-        for (int i = 0; i < 32; i++) {
-            const int g = wave + 16 * i;
-            const uint32_t c = sh.h[g * 64 + lane];
-            sum += (c & 0xFFFFu) + (c >> 16);
-            uint32_t pos, neg;
-            cleaned(g * 64 + lane, c, pos, neg);
-            const uint64_t mp = __ballot(pos != 0), mn = __ballot(neg != 0);
-            if (mp) {
-                pg |= 1u << i;
-                top = min(top, (uint32_t)((511 - g) * 64 + __builtin_clzll(mp)));
-            }
-            if (mn) {
-                ng |= 1u << i;
-                top = min(top, (uint32_t)(32768 + g * 64 + __builtin_ctzll(mn)));
-            }
-        }
-        if (sum_up) {
-            if (wave == 0) sum += (sh.dummy[lane] & 0xFFFFu) + (sh.dummy[lane] >> 16);
-            sum = (uint32_t)wave_scan((int)sum);
-            if (lane == 63) atomicAdd(&sh.counted, sum);
-        }
-        if (lane == 0) atomicMin(&sh.top_pos, top);
-    }
-
-    // Totals of the blocks of the surveyed groups.
-    __device__ void total(uint32_t pg, uint32_t ng) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        uint32_t any = pg | ng;
-        while (any) {
-            const int i = __builtin_ctz(any);
-            any &= any - 1;
-            const int g = wave + 16 * i;
-            uint32_t pos, neg;
-            cleaned(g * 64 + lane, sh.h[g * 64 + lane], pos, neg);
-            if ((pg >> i) & 1) put(511 - g, pos, bits_value(g * 64 + lane));
-            if ((ng >> i) & 1) put(512 + g, neg, bits_value(0x8000 + g * 64 + lane));
-        }
-    }
-    __device__ __forceinline__ void put(int b, uint32_t c, float value) {
-        const uint32_t cs = (uint32_t)wave_scan((int)c);
-        const double ms = wave_scan(c ? (double)c * weight(value) : 0.0);
-        if ((threadIdx.x & 63) == 63) {
-            sh.blk_cnt[b] = cs;
-            sh.blk_mass[b] = ms;
-        }
-    }
-
     // Block b's counts in h (a row counted one sign at a time holds one).
     __device__ __forceinline__ void hold(int b) {
-        if (wide >= 0 && wide != (b >= 512)) recount(b >= 512);  // uniform
-    }
-    __device__ void recount(int sign) {
-        __syncthreads();
-        clear(sh);
-        __syncthreads();
-        wide = sign;
-        for (int i = threadIdx.x; i < row.V; i += kRowThreads) {
-            if (row.mask && !((row.mask[i >> 6] >> (i & 63)) & 1)) continue;
-            const uint32_t v = row.x[i];
-            if (v >= 0xFF80u || (v > 0x8000u) != (sign != 0)) continue;
-            atomicAdd(&sh.h[v & 0x7FFFu], 1u);
+        if (wide >= 0 && wide != (b >= kHistBlocks / 2)) {  // uniform
+            wide = b >= kHistBlocks / 2;
+            recount(sh, row.x, row.mask, row.V, wide);
         }
-        __syncthreads();
     }
 };
+
+// Launches KERNEL<NP, SPANS> with as many pieces as rows of V ids need (7: the
+// largest skew).  20 pieces are 80 of a thread's 128 registers; beyond that,
+// spans of 16.
+#define CG_LAUNCH_ROWS(KERNEL, V, BATCH, STREAM, ARGS)                                              \
+    do {                                                                                            \
+        const int pieces_ = ((V) + 7 + kPieceIds - 1) / kPieceIds;                                  \
+        const dim3 grid_(BATCH), block_(kRowThreads);                                               \
+        if (pieces_ <= 4) hipLaunchKernelGGL((KERNEL<4, false>), grid_, block_, 0, STREAM, ARGS);   \
+        else if (pieces_ <= 8) hipLaunchKernelGGL((KERNEL<8, false>), grid_, block_, 0, STREAM, ARGS);   \
+        else if (pieces_ <= 16) hipLaunchKernelGGL((KERNEL<16, false>), grid_, block_, 0, STREAM, ARGS); \
+        else if (pieces_ <= 20) hipLaunchKernelGGL((KERNEL<20, false>), grid_, block_, 0, STREAM, ARGS); \
+        else hipLaunchKernelGGL((KERNEL<16, true>), grid_, block_, 0, STREAM, ARGS);                \
+    } while (0)
 
 }  // namespace cg

@@ -48,13 +48,45 @@ struct RowView {
     }
 };
 
-// Weight of a candidate under temperature: 2^0 at the maximum.
+// e^y for y <= 0 (and a little above) to within two units of a double's last
+// place; 0 for NaN.  y = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts, so
+// that r is exact), e^r by its power series to r^13 / 13! (the next term is
+// under 2^-57), times 2^n.
+//
+// Its constants are put into scalar registers where they are used: kept in
+// vector registers over the kernels' loops they are 30 of a thread's 128.
+__device__ __forceinline__ double scalar(double c) {
+    asm volatile("" : "+s"(c));
+    return c;
+}
+__device__ __forceinline__ double exp_falling(double y) {
+    y = fmax(y, -2000.0);  // under every double; NaN comes out of this as -2000
+    const double n = rint(y * scalar(1.4426950408889634074));
+    double r = fma(-n, scalar(6.93147180369123816490e-01), y);
+    r = fma(-n, scalar(1.90821492927058770002e-10), r);
+    double p = scalar(1.0 / 6227020800.0);
+    p = fma(p, r, scalar(1.0 / 479001600.0));
+    p = fma(p, r, scalar(1.0 / 39916800.0));
+    p = fma(p, r, scalar(1.0 / 3628800.0));
+    p = fma(p, r, scalar(1.0 / 362880.0));
+    p = fma(p, r, scalar(1.0 / 40320.0));
+    p = fma(p, r, scalar(1.0 / 5040.0));
+    p = fma(p, r, scalar(1.0 / 720.0));
+    p = fma(p, r, scalar(1.0 / 120.0));
+    p = fma(p, r, scalar(1.0 / 24.0));
+    p = fma(p, r, scalar(1.0 / 6.0));
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return ldexp(p, (int)n);
+}
+
+// Weight of a candidate under temperature: 1 at the maximum.  Where m = +inf
+// meets T = +inf the exponent is NaN: all weight is m's.
 struct Weight {
     double m, inv_t;  // largest logit; 1 / T (1 for greedy rows)
     __device__ __forceinline__ double operator()(float x) const {
-        if ((double)x == m) return 1.0;
-        const double y = ((double)x - m) * inv_t;
-        return y == y ? exp(y) : 0.0;  // m = +inf under T = +inf: all weight is m's
+        return (double)x == m ? 1.0 : exp_falling(((double)x - m) * inv_t);
     }
 };
 constexpr double kMassUnit = 0x1p40;

@@ -133,30 +133,35 @@ __device__ void write_top(uint64_t *list, uint32_t n, const TopArgs &a, int r, V
 
 // bfloat16 rows: one read, the k-th value from the counts (row_hist.hpp),
 // then the candidates down to it from the registers.
-template <int NP>
+template <int NP, bool SPANS>
 __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
     __shared__ HistShared sh;
     const int r = blockIdx.x;
-    HistRow<NP> row;
+    HistRow<NP, SPANS> row;
     row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
              a.wpr, a.V);
-    HistOrder<NP> order(sh, row);
+    HistOrder<NP, SPANS> order(sh, row);
     uint64_t *list = (uint64_t *)sh.h;
     uint32_t n = 0;
     if (order.build(1.0)) {
-        const HistPlace q = order.template find<0>((uint32_t)a.k - 1, 0.0);
-        const double mass = order.total_mass();
-        if (threadIdx.x == 0) a.lse[r] = (float)(order.weight.m + log(mass));
+        if (order.searches()) {
+            const HistPlace q = order.template find<0>((uint32_t)a.k - 1, 0.0);
+            const double mass = order.total_mass();
+            if (threadIdx.x == 0) {
+                sh.place = q;
+                sh.n_list = 0;
+                a.lse[r] = (float)(order.weight.m + log(mass));
+            }
+        }
+        __syncthreads();
+        const HistPlace q = sh.place;
         // every tie of the last value when they fit, else only the larger
         // candidates here and as many ties as are wanted by their ids
         const bool all = q.above + q.count <= kListRoom;
-        __syncthreads();
-        if (threadIdx.x == 0) sh.n_list = 0;
-        __syncthreads();
         const int n_spans = row.spans();
         for (int s = 0; s < n_spans; s++) {
             const int span = (row.span_at + (s ? 1 : 0)) % n_spans;  // the one in the registers first
-            if (s) row.load(span, sh.lut, [] {});
+            if (s) row.load(span, sh.lut);
             if (all || q.pos) row.collect(all ? q.pos : q.pos - 1, list, kListRoom, sh);
         }
         if (all) {
@@ -170,13 +175,6 @@ __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
     }
     __syncthreads();
     write_top(list, n, a, r, [](uint32_t pos) { return bits_value(pos_bits(pos)); });
-}
-
-void launch_counts(const TopArgs &a, int batch, hipStream_t st) {
-    const int pieces = (a.V + 7 + kPieceIds - 1) / kPieceIds;  // 7: the largest skew
-    if (pieces <= 4) hipLaunchKernelGGL((k_top_counts<4>), dim3(batch), dim3(kRowThreads), 0, st, a);
-    else if (pieces <= 8) hipLaunchKernelGGL((k_top_counts<8>), dim3(batch), dim3(kRowThreads), 0, st, a);
-    else hipLaunchKernelGGL((k_top_counts<kMaxPieces>), dim3(batch), dim3(kRowThreads), 0, st, a);
 }
 
 }  // namespace
@@ -214,7 +212,7 @@ int cg_top_logits(const void *d_logits, int32_t dtype, int32_t batch, int32_t vo
     if (dtype == 0)
         hipLaunchKernelGGL((k_top_logits<0>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
     else
-        launch_counts(a, batch, (hipStream_t)stream);
+        CG_LAUNCH_ROWS(k_top_counts, vocab, batch, (hipStream_t)stream, a);
     return launch_status("top_logits");
 }
 
