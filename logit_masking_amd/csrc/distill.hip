@@ -7,19 +7,17 @@
 #include <algorithm>
 
 #include "cg_internal.hpp"
+#include "row_select.hpp"
 
 namespace cg {
 
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kNumWaves = kThreads / 64;
-static_assert(CG_MAX_TOP <= kThreads, "one thread per teacher entry");
-
 // A saved normaliser L is rounded to |L| 2^-24, and q by as much: one above
 // this (logits at a type's lowest value, say) is not used, the row is summed
 // again.
 constexpr float kSavedMax = 1024.f;
+constexpr int kPolicy = 0;
 
 struct DistillArgs {
     const void *logits;
@@ -37,6 +35,7 @@ struct DistillArgs {
     int64_t grad_stride;
 };
 
+// ---- single elements ----------------------------------------------------------
 template <int DT>
 __device__ __forceinline__ float load_x(const void *p, size_t i) {
     if (DT == 0) return ((const float *)p)[i];
@@ -54,7 +53,9 @@ __device__ __forceinline__ void store_x(void *p, size_t i, float v) {
     }
 }
 
-template <class T, class F>
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+template <int WAVES, class T, class F>
 __device__ T block_reduce(T v, T *slots, F op) {
 #pragma unroll
     for (int d = 32; d; d >>= 1) v = op(v, __shfl_xor(v, d));
@@ -62,98 +63,383 @@ __device__ T block_reduce(T v, T *slots, F op) {
     if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
     __syncthreads();
     v = slots[0];
-    for (int w = 1; w < kNumWaves; w++) v = op(v, slots[w]);
+#pragma unroll
+    for (int w = 1; w < WAVES; w++) v = op(v, slots[w]);
     return v;
 }
 
+// ---- the row in 16-byte pieces ------------------------------------------------
+// Piece q of the row lies on a 16-byte boundary: a row that starts past one by
+// `skew` elements is read from the boundary, what lies before its start is
+// never used.
+constexpr int kBufWord3 = 0x00020000;  // raw buffer, 32-bit data format
+
 template <int DT>
-__global__ __launch_bounds__(kThreads) void k_distill_topk(DistillArgs a) {
-    __shared__ double dslots[kNumWaves];
-    __shared__ float fslots[kNumWaves];
+struct Pieces {
+    static constexpr int kN = DT == 0 ? 4 : 8;  // elements of a piece
+    static constexpr int kEs = DT == 0 ? 4 : 2;
+    static constexpr uint32_t kAll = (1u << kN) - 1u;
+    __amdgpu_buffer_rsrc_t rx, rm;
+    char *out;  // the gradient's row
+    int V, skew;
+    bool masked, aligned_out;  // the gradient's pieces lie on boundaries too
+
+    __device__ __forceinline__ Pieces(const char *row, const uint64_t *mask, char *grad, int vocab)
+        : out(grad), V(vocab), masked(mask != nullptr) {
+        skew = (int)(((uintptr_t)row & 15) / kEs);
+        aligned_out = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
+        rx = __builtin_amdgcn_make_buffer_rsrc((void *)(row - skew * kEs), (short)0, ((V + skew) * kEs + 3) & ~3, kBufWord3);
+        rm = __builtin_amdgcn_make_buffer_rsrc((void *)mask, (short)0, mask ? (vocab + 63) / 64 * 8 : 0, kBufWord3);
+    }
+    __device__ __forceinline__ int count() const { return (V + skew + kN - 1) / kN; }
+    __device__ __forceinline__ int first(int q) const { return q * kN - skew; }  // id of its first element
+
+    // The mask's bits around piece q as they lie, then those of its elements
+    // that are in the row and allowed.
+    __device__ __forceinline__ uint32_t ask_mask(int q) const {
+        if (!masked) return 0xFFFFu;
+        const int at = first(q) >> 3;
+        uint32_t b = __builtin_amdgcn_raw_buffer_load_b8(rm, at, 0, 0);
+        if (skew) b |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rm, at + 1, 0, 0) << 8;
+        return b;
+    }
+    __device__ __forceinline__ uint32_t usable(int q, uint32_t raw) const {
+        const int f = first(q), left = V - f;
+        uint32_t b = (masked ? raw >> (f & 7) : raw) & kAll;
+        if (f < 0) b &= kAll << -f;
+        return left >= kN ? b : left <= 0 ? 0u : b & ((1u << left) - 1u);
+    }
+    // A piece without a usable element asks past the buffer's end, which reads
+    // nothing; without a branch, so that loads stay in flight together.
+    __device__ __forceinline__ uint4 ask(int q, uint32_t use) const {
+        return __builtin_bit_cast(uint4,
+                                  __builtin_amdgcn_raw_buffer_load_b128(rx, use ? q * 16 : 0x7FFFFFF0, 0, kPolicy));
+    }
+    // -inf in place of what is not usable (bfloat16: lut holds the pair
+    // selects of a byte).
+    __device__ __forceinline__ uint4 select(uint4 v, uint32_t use, const uint4 *lut) const {
+        if (DT == 1) {
+            const uint4 s = lut[use];
+            v.x = (v.x & s.x) | (~s.x & 0xFF80FF80u);
+            v.y = (v.y & s.y) | (~s.y & 0xFF80FF80u);
+            v.z = (v.z & s.z) | (~s.z & 0xFF80FF80u);
+            v.w = (v.w & s.w) | (~s.w & 0xFF80FF80u);
+        } else {
+            v.x = use & 1 ? v.x : 0xFF800000u;
+            v.y = use & 2 ? v.y : 0xFF800000u;
+            v.z = use & 4 ? v.z : 0xFF800000u;
+            v.w = use & 8 ? v.w : 0xFF800000u;
+        }
+        return v;
+    }
+    static __device__ __forceinline__ void floats(uint4 v, float (&x)[kN]) {
+        const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < kN; j++)
+            x[j] = __uint_as_float(DT == 0 ? d[j] : (j & 1) ? d[j / 2] & 0xFFFF0000u : d[j / 2] << 16);
+    }
+
+    // Writes piece q of the gradient: the elements that are in the row.
+    __device__ __forceinline__ void put(int q, const float (&g)[kN]) const {
+        const int f = first(q);
+        uint32_t d[4];
+        if (DT == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) d[j] = __float_as_uint(g[j]);
+        } else {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            typedef float f32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+            for (int j = 0; j < 4; j++)  // to nearest, ties to even
+                d[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){g[2 * j], g[2 * j + 1]}, bf16x2));
+        }
+        if (aligned_out && f >= 0 && f + kN <= V) {
+            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+            __builtin_nontemporal_store((u32x4){d[0], d[1], d[2], d[3]}, (u32x4 *)(out + (size_t)f * kEs));
+        } else {
+#pragma unroll
+            for (int j = 0; j < kN; j++) {
+                if (f + j < 0 || f + j >= V) continue;
+                if (DT == 0) ((uint32_t *)out)[f + j] = d[j];
+                else ((uint16_t *)out)[f + j] = (uint16_t)(d[j / 2] >> (16 * (j & 1)));
+            }
+        }
+    }
+};
+
+// Running maximum and sum of 2^((x - m) kk) of a thread's elements.  (The
+// difference first: x kk alone overflows at a type's lowest value.)
+struct Running {
+    float m, s;
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N], float kk) {
+        float top = x[0];
+#pragma unroll
+        for (int j = 1; j < N; j++) top = fmaxf(top, x[j]);
+        if (top > m) {
+            s *= exp2_fast((m - top) * kk);
+            m = top;
+        }
+        const float base = m == -INFINITY ? 0.f : m;  // only -inf so far
+        float part = exp2_fast((x[0] - base) * kk);
+#pragma unroll
+        for (int j = 1; j < N; j++) part += exp2_fast((x[j] - base) * kk);
+        s += part;
+    }
+};
+
+// The gradient from an element: scale 2^((x - base) kk - l2s), 0 for -inf.
+struct Slope {
+    float kk, base, l2s, scale;
+    bool plain;  // -inf comes out as 0 by itself: no NaN, no infinity among the above
+    template <int N>
+    __device__ __forceinline__ void operator()(const float (&x)[N], float (&g)[N]) const {
+#pragma unroll
+        for (int j = 0; j < N; j++) g[j] = exp2_fast(fmaf(x[j] - base, kk, -l2s)) * scale;
+        if (!plain) {
+#pragma unroll
+            for (int j = 0; j < N; j++) g[j] = x[j] == -INFINITY ? 0.f : g[j];
+        }
+    }
+};
+
+// One row a workgroup.  HELD pieces a thread in registers between the sum and
+// the gradient (0: the row is read again for it).
+template <int DT, int THREADS, int HELD>
+__global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
+    typedef Pieces<DT> P;
+    constexpr int kWaves = THREADS / 64, kN = P::kN;
+    constexpr int kEntries = (CG_MAX_TOP + THREADS - 1) / THREADS;  // teacher entries a thread
+    constexpr int kAhead = 4;                                      // pieces a thread asks for together
+    __shared__ double dslots[kWaves];
+    __shared__ float fslots[kWaves];
     __shared__ float p_of[CG_MAX_TOP];
     __shared__ int id_of[CG_MAX_TOP];
+    __shared__ uint4 lut[DT == 1 ? 256 : 1];
     const int r = blockIdx.x, t = threadIdx.x;
-    const char *x = (const char *)a.logits + (size_t)r * (size_t)a.stride * (DT == 0 ? 4 : 2);
+    const char *x = (const char *)a.logits + (size_t)r * (size_t)a.stride * P::kEs;
     const uint64_t *mask = a.mask ? a.mask + (size_t)r * a.wpr : nullptr;
+    char *g = a.grad ? (char *)a.grad + (size_t)r * (size_t)a.grad_stride * P::kEs : nullptr;
+    const P row(x, mask, g, a.V);
+    const int n_pieces = row.count();
     auto fmax_op = [](float p, float q) { return fmaxf(p, q); };
     auto sum_op = [](double p, double q) { return p + q; };
-    auto logit = [&](int i) -> float {  // -inf: not a candidate
-        return !mask || ((mask[i >> 6] >> (i & 63)) & 1) ? load_x<DT>(x, i) : -INFINITY;
-    };
     const float kk = (float)(1.4426950408889634 / (double)a.tau);
+    if (DT == 1) {
+        for (int v = t; v < 256; v += THREADS) {
+            uint32_t m[4];
+#pragma unroll
+            for (int p = 0; p < 4; p++)
+                m[p] = ((v >> (2 * p)) & 1 ? 0x0000FFFFu : 0u) | ((v >> (2 * p + 1)) & 1 ? 0xFFFF0000u : 0u);
+            lut[v] = make_uint4(m[0], m[1], m[2], m[3]);
+        }
+        __syncthreads();
+    }
 
     // the normaliser: L = m / tau + ln sum 2^((x - m) kk), kept apart as m and
     // log2 of the sum; a saved one stands for a sum of 1 at m = 0
     double L, ln_sum = 0.0;
     float base = 0.f, l2s;
     const float saved = a.lse_in ? a.lse_in[r] : INFINITY;
-    if (fabsf(saved) <= kSavedMax) {
+    uint4 d[HELD ? HELD : 1];
+    if (HELD == 0 && fabsf(saved) <= kSavedMax) {
         L = (double)saved;
         l2s = (float)(L * 1.4426950408889634);
     } else {
-        float m = -INFINITY, s = 0.f;
-        for (int i = t; i < a.V; i += kThreads) {
-            const float v = logit(i);
-            if (v > m) {
-                s *= exp2f((m - v) * kk);
-                m = v;
+        Running run{-INFINITY, 0.f};
+        if (HELD) {
+            uint32_t use[HELD ? HELD : 1];
+#pragma unroll
+            for (int i = 0; i < HELD; i++) use[i] = row.ask_mask(t + i * THREADS);
+#pragma unroll
+            for (int i = 0; i < HELD; i++) {
+                use[i] = row.usable(t + i * THREADS, use[i]);
+                d[i] = row.ask(t + i * THREADS, use[i]);
             }
-            if (v != -INFINITY) s += v == m ? 1.f : exp2f((v - m) * kk);
+#pragma unroll
+            for (int i = 0; i < HELD; i++) {
+                if (!__any(use[i] != 0)) {
+                    d[i] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+                    if (DT == 0) d[i] = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+                    continue;
+                }
+                if (__any(use[i] != P::kAll)) d[i] = row.select(d[i], use[i], lut);
+                float v[kN];
+                P::floats(d[i], v);
+                run.add(v, kk);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            for (int q0 = t; q0 < n_pieces; q0 += kAhead * THREADS) {
+                uint32_t use[kAhead];
+                uint4 v4[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; i++) use[i] = row.ask_mask(q0 + i * THREADS);
+#pragma unroll
+                for (int i = 0; i < kAhead; i++) {
+                    use[i] = row.usable(q0 + i * THREADS, use[i]);
+                    v4[i] = row.ask(q0 + i * THREADS, use[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; i++) {
+                    if (!__any(use[i] != 0)) continue;
+                    if (__any(use[i] != P::kAll)) v4[i] = row.select(v4[i], use[i], lut);
+                    float v[kN];
+                    P::floats(v4[i], v);
+                    run.add(v, kk);
+                }
+            }
         }
-        const float best = block_reduce(m, fslots, fmax_op);
-        double part = m == best ? (double)s : (double)s * exp2((double)(m - best) * (double)kk);
-        if (s == 0.f) part = 0.0;
-        const double sum = block_reduce(part, dslots, sum_op);
+        const float best = block_reduce<kWaves>(run.m, fslots, fmax_op);
+        // (a thread that saw only -inf, or a NaN beside nothing else, has no maximum to scale from)
+        const double part = run.m == best ? (double)run.s : run.s == 0.f ? 0.0 : (double)run.s * exp_falling(((double)run.m - (double)best) / (double)a.tau);
+        const double sum = block_reduce<kWaves>(part, dslots, sum_op);
         ln_sum = log(sum);
         L = (double)best / (double)a.tau + ln_sum;
         base = best;
-        l2s = (float)log2(sum);
+        l2s = (float)(ln_sum * 1.4426950408889634);
     }
 
     // the teacher's distribution over the entries the student can take
-    int id = -1;
-    float s_id = -INFINITY, tl = -INFINITY;
-    if (t < a.k) {
-        id = a.t_ids[(size_t)r * a.k + t];
-        if (id >= 0 && id < a.V) {
-            s_id = logit(id);
-            if (s_id != -INFINITY) tl = a.t_logits[(size_t)r * a.k + t];
+    int id[kEntries];
+    float s_id[kEntries], tl[kEntries];
+    double p[kEntries];
+    float tmax = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kEntries; i++) {
+        const int e = t + i * THREADS;
+        id[i] = -1;
+        s_id[i] = tl[i] = -INFINITY;
+        if (e < a.k) {
+            id[i] = a.t_ids[(size_t)r * a.k + e];
+            if (id[i] >= 0 && id[i] < a.V) {
+                if (!mask || ((mask[id[i] >> 6] >> (id[i] & 63)) & 1)) s_id[i] = load_x<DT>(x, id[i]);
+                if (s_id[i] != -INFINITY) tl[i] = a.t_logits[(size_t)r * a.k + e];
+            }
         }
+        tmax = fmaxf(tmax, tl[i]);
     }
-    const float tmax = block_reduce(tl, fslots, fmax_op);
+    tmax = block_reduce<kWaves>(tmax, fslots, fmax_op);
     const bool some = tmax > -INFINITY;
-    const double e = tl > -INFINITY ? exp(((double)tl - (double)tmax) / (double)a.tau) : 0.0;
-    const double esum = block_reduce(e, dslots, sum_op);
-    const double p = some ? e / esum : 0.0;
+    double esum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kEntries; i++) {
+        p[i] = tl[i] > -INFINITY ? exp_falling(((double)tl[i] - (double)tmax) / (double)a.tau) : 0.0;
+        esum += p[i];
+    }
+    esum = block_reduce<kWaves>(esum, dslots, sum_op);
+    const double ln_esum = log(esum);
+    double loss = 0.0;
+#pragma unroll
+    for (int i = 0; i < kEntries; i++) {
+        p[i] = some ? p[i] / esum : 0.0;
+        if (a.loss && p[i] > 0.0)
+            loss += p[i] * ((((double)tl[i] - (double)tmax) - ((double)s_id[i] - (double)base)) / (double)a.tau - ln_esum +
+                            ln_sum);
+    }
     if (a.loss) {
-        const double term = p > 0.0 ? p * ((((double)tl - (double)tmax) - ((double)s_id - (double)base)) / (double)a.tau -
-                                         log(esum) + ln_sum)
-                                  : 0.0;
-        const double loss = block_reduce(term, dslots, sum_op);
+        loss = block_reduce<kWaves>(loss, dslots, sum_op);
         if (t == 0) a.loss[r] = (float)((double)a.tau * (double)a.tau * loss);
     }
     if (a.lse && t == 0) a.lse[r] = (float)L;
-    if (!a.grad) return;
+    if (!g) return;
 
-    // d loss / d x_v = tau (q_v - p_v), q_v = 2^((x - base) kk - l2s)
-    char *g = (char *)a.grad + (size_t)r * (size_t)a.grad_stride * (DT == 0 ? 4 : 2);
+    // d loss / d x_v = tau (q_v - p_v): first the q everywhere
     const double scale = some ? (double)a.weight[r] * (double)a.tau : 0.0;
-    const float fs = (float)scale;
-    for (int i = t; i < a.V; i += kThreads) {
-        const float v = logit(i);
-        store_x<DT>(g, i, v == -INFINITY || !some ? 0.f : exp2f(fmaf(v - base, kk, -l2s)) * fs);
+    Slope slope{kk, base, l2s, (float)scale, false};
+    slope.plain = fabsf(base) < INFINITY && fabsf(l2s) < INFINITY && fabsf(slope.scale) < INFINITY;
+    auto zeros = [&](int q) {
+        float z[kN];
+#pragma unroll
+        for (int j = 0; j < kN; j++) z[j] = 0.f;
+        row.put(q, z);
+    };
+    if (!some) {  // nothing recorded, or nothing allowed
+        for (int q = t; q < n_pieces; q += THREADS) zeros(q);
+        return;
     }
-    if (t < a.k) {
-        id_of[t] = p > 0.0 ? id : -1;
-        p_of[t] = (float)p;
+    if (HELD) {
+#pragma unroll
+        for (int i = 0; i < HELD; i++) {
+            const int q = t + i * THREADS;
+            if (q < n_pieces) {
+                float v[kN], o[kN];
+                P::floats(d[i], v);
+                slope(v, o);
+                row.put(q, o);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else {
+        for (int q0 = t; q0 < n_pieces; q0 += kAhead * THREADS) {
+            uint32_t use[kAhead];
+            uint4 v4[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) use[i] = row.ask_mask(q0 + i * THREADS);
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) {
+                use[i] = row.usable(q0 + i * THREADS, use[i]);
+                v4[i] = row.ask(q0 + i * THREADS, use[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) {
+                const int q = q0 + i * THREADS;
+                if (q >= n_pieces) continue;
+                if (!__any(use[i] != 0)) {
+                    zeros(q);
+                    continue;
+                }
+                if (__any(use[i] != P::kAll)) v4[i] = row.select(v4[i], use[i], lut);
+                float v[kN], o[kN];
+                P::floats(v4[i], v);
+                slope(v, o);
+                row.put(q, o);
+            }
+        }
     }
-    __syncthreads();  // and the row's stores are done before the entries' are written over them
-    if (t < a.k && p > 0.0) {
-        double sum = 0.0;
-        for (int j = 0; j < a.k; j++) sum += id_of[j] == id ? (double)p_of[j] : 0.0;
-        const double q = exp2(((double)s_id - (double)base) / (double)a.tau * 1.4426950408889634 - (double)l2s);
-        store_x<DT>(g, id, (float)((q - sum) * scale));
+    // then the entries' places, over what was just written
+#pragma unroll
+    for (int i = 0; i < kEntries; i++) {
+        const int e = t + i * THREADS;
+        if (e < a.k) {
+            id_of[e] = p[i] > 0.0 ? id[i] : -1;
+            p_of[e] = (float)p[i];
+        }
     }
+    __syncthreads();  // the row's stores are done as well
+#pragma unroll
+    for (int i = 0; i < kEntries; i++) {
+        if (p[i] > 0.0) {
+            double sum = 0.0;
+            for (int j = 0; j < a.k; j++) sum += id_of[j] == id[i] ? (double)p_of[j] : 0.0;
+            const double y = ((double)s_id[i] - (double)base) / (double)a.tau - (HELD == 0 && fabsf(saved) <= kSavedMax ? L : ln_sum);
+            const double q = y == y ? exp_falling(y) : y;
+            store_x<DT>(g, id[i], (float)((q - sum) * scale));
+        }
+    }
+}
+
+template <int DT>
+void launch_rows(const DistillArgs &a, int rows, hipStream_t st) {
+    constexpr int kN = Pieces<DT>::kN;
+    const int pieces = (a.V + kN - 1 + kN - 1) / kN;  // with the largest skew
+    const dim3 grid(rows);
+    // both directions hold the row in registers while it fits
+    if (a.grad && !a.lse_in) {
+        if (pieces <= 4 * 1024) {
+            hipLaunchKernelGGL((k_distill_topk<DT, 1024, 4>), grid, dim3(1024), 0, st, a);
+            return;
+        }
+        if (pieces <= 8 * 1024) {
+            hipLaunchKernelGGL((k_distill_topk<DT, 1024, 8>), grid, dim3(1024), 0, st, a);
+            return;
+        }
+        if (pieces <= 16 * 1024) {
+            hipLaunchKernelGGL((k_distill_topk<DT, 1024, 16>), grid, dim3(1024), 0, st, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_distill_topk<DT, 512, 0>), grid, dim3(512), 0, st, a);
 }
 
 }  // namespace
@@ -177,10 +463,8 @@ static int distill_launch(const DistillArgs &a, int32_t dtype, int32_t rows, voi
     if (a.grad && a.grad_stride < a.V) return distill_arg_error("grad_stride < vocab");
     if (rows == 0) return CG_OK;
     if (!a.logits || !a.t_ids || !a.t_logits || (a.grad && !a.weight)) return distill_arg_error("NULL device pointer");
-    if (dtype == 0)
-        hipLaunchKernelGGL((k_distill_topk<0>), dim3(rows), dim3(kThreads), 0, (hipStream_t)stream, a);
-    else
-        hipLaunchKernelGGL((k_distill_topk<1>), dim3(rows), dim3(kThreads), 0, (hipStream_t)stream, a);
+    if (dtype == 0) launch_rows<0>(a, rows, (hipStream_t)stream);
+    else launch_rows<1>(a, rows, (hipStream_t)stream);
     return launch_status("distill_topk");
 }
 
