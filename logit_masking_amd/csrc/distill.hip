@@ -62,9 +62,9 @@ __device__ T block_reduce(T v, T *slots, F op) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = slots[0];
+    v = slots[threadIdx.x & (WAVES - 1)];
 #pragma unroll
-    for (int w = 1; w < WAVES; w++) v = op(v, slots[w]);
+    for (int d = WAVES / 2; d; d >>= 1) v = op(v, __shfl_xor(v, d));
     return v;
 }
 
@@ -248,25 +248,25 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
     } else {
         Running run{-INFINITY, 0.f};
         if (HELD) {
-            uint32_t use[HELD ? HELD : 1];
+            uint32_t use[HELD ? HELD : 1], bytes[(HELD + 3) / 4 + 1];  // four pieces' bits a word
 #pragma unroll
             for (int i = 0; i < HELD; i++) use[i] = row.ask_mask(t + i * THREADS);
 #pragma unroll
             for (int i = 0; i < HELD; i++) {
-                use[i] = row.usable(t + i * THREADS, use[i]);
-                d[i] = row.ask(t + i * THREADS, use[i]);
+                const uint32_t b = row.usable(t + i * THREADS, use[i]);
+                d[i] = row.ask(t + i * THREADS, b);
+                bytes[i / 4] = (i % 4 ? bytes[i / 4] : 0u) | b << (8 * (i % 4));
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < HELD; i++) {
-                if (!__any(use[i] != 0)) {
-                    d[i] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
-                    if (DT == 0) d[i] = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-                    continue;
+                const uint32_t b = (bytes[i / 4] >> (8 * (i % 4))) & 0xFFu;
+                if (__any(b != P::kAll)) d[i] = row.select(d[i], b, lut);
+                if (__any(b != 0)) {
+                    float v[kN];
+                    P::floats(d[i], v);
+                    run.add(v, kk);
                 }
-                if (__any(use[i] != P::kAll)) d[i] = row.select(d[i], use[i], lut);
-                float v[kN];
-                P::floats(d[i], v);
-                run.add(v, kk);
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
         // (a thread that saw only -inf, or a NaN beside nothing else, has no maximum to scale from)
         const double part = run.m == best ? (double)run.s : run.s == 0.f ? 0.0 : (double)run.s * exp_falling(((double)run.m - (double)best) / (double)a.tau);
         const double sum = block_reduce<kWaves>(part, dslots, sum_op);
-        ln_sum = log(sum);
+        ln_sum = log_of(sum);
         L = (double)best / (double)a.tau + ln_sum;
         base = best;
         l2s = (float)(ln_sum * 1.4426950408889634);
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
         esum += p[i];
     }
     esum = block_reduce<kWaves>(esum, dslots, sum_op);
-    const double ln_esum = log(esum);
+    const double ln_esum = log_of(esum);
     double loss = 0.0;
 #pragma unroll
     for (int i = 0; i < kEntries; i++) {

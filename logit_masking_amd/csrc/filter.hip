@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_sample(FilterArgs a) {
         const float x = value_of_key(pick_key);
         const double y = (double)x == weight.m ? 0.0 : ((double)x - weight.m) * weight.inv_t;
         a.ids[r] = id;
-        a.logprob[r] = (float)(y - log((double)mass / kMassUnit));
+        a.logprob[r] = (float)(y - log_of((double)mass / kMassUnit));
     }
 }
 
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
         const double x = (double)bits_value(pos_bits(pos));
         const double y = x == order.weight.m ? 0.0 : (x - order.weight.m) * order.weight.inv_t;
         a.ids[r] = id;
-        a.logprob[r] = (float)(y - log(mass));
+        a.logprob[r] = (float)(y - log_of(mass));
     }
 }
 

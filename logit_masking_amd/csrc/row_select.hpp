@@ -81,6 +81,33 @@ __device__ __forceinline__ double exp_falling(double y) {
     return ldexp(p, (int)n);
 }
 
+// ln s to within a few units of a double's last place; -inf for 0, NaN for
+// NaN.  s = 2^e f with f in [sqrt(1/2), sqrt(2)), and with z = (f - 1) / (f + 1)
+// ln f = 2 (z + z^3 / 3 + z^5 / 5 + ...): |z| < 0.172, so the term after
+// z^21 / 21 is under 2^-57.
+__device__ __forceinline__ double log_of(double s) {
+    if (s == 0.0) return -INFINITY;
+    double f = __builtin_amdgcn_frexp_mant(s);  // [1/2, 1)
+    int e = __builtin_amdgcn_frexp_exp(s);
+    if (f < 0.70710678118654752) {
+        f *= 2.0;
+        e--;
+    }
+    const double z = (f - 1.0) / (f + 1.0), y = z * z;
+    double p = scalar(1.0 / 21.0);
+    p = fma(p, y, scalar(1.0 / 19.0));
+    p = fma(p, y, scalar(1.0 / 17.0));
+    p = fma(p, y, scalar(1.0 / 15.0));
+    p = fma(p, y, scalar(1.0 / 13.0));
+    p = fma(p, y, scalar(1.0 / 11.0));
+    p = fma(p, y, scalar(1.0 / 9.0));
+    p = fma(p, y, scalar(1.0 / 7.0));
+    p = fma(p, y, scalar(1.0 / 5.0));
+    p = fma(p, y, scalar(1.0 / 3.0));
+    p = fma(p * y, z, z);
+    return fma((double)e, scalar(0.693147180559945309), 2.0 * p);
+}
+
 // Weight of a candidate under temperature: 1 at the maximum.  Where m = +inf
 // meets T = +inf the exponent is NaN: all weight is m's.
 struct Weight {

@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kRowThreads) void k_top_logits(TopArgs a) {
             __syncthreads();
         }
         sort_falling(list, n_pow);
-        if (threadIdx.x == 0) a.lse[r] = (float)(weight.m + log((double)mass / kMassUnit));
+        if (threadIdx.x == 0) a.lse[r] = (float)(weight.m + log_of((double)mass / kMassUnit));
     } else if (threadIdx.x == 0) {
         a.lse[r] = -INFINITY;
     }
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
             if (threadIdx.x == 0) {
                 sh.place = q;
                 sh.n_list = 0;
-                a.lse[r] = (float)(order.weight.m + log(mass));
+                a.lse[r] = (float)(order.weight.m + log_of(mass));
             }
         }
         __syncthreads();
