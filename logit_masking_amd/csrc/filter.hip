@@ -7,8 +7,7 @@
 #include <algorithm>
 
 #include "cg_internal.hpp"
-#include "row_hist.hpp"
-#include "row_select.hpp"
+#include "row_fine.hpp"
 
 namespace cg {
 
@@ -32,10 +31,10 @@ struct FilterArgs {
 struct Cut {
     uint32_t key, ties;
 };
+// The whole draw digit by digit (row_select.hpp), for rows that the windows do
+// not take: a bin of float32 logits with more candidates than a window.
 template <int DT>
-__global__ __launch_bounds__(kRowThreads) void k_filter_sample(FilterArgs a) {
-    __shared__ SelectShared sh;
-    const int r = blockIdx.x;
+__device__ void filter_by_digits(const FilterArgs &a, int r, SelectShared &sh) {
     RowView<DT> row{(const char *)a.logits + (size_t)r * (size_t)a.stride * (DT == 0 ? 4 : 2),
                     a.mask ? a.mask + (size_t)r * a.wpr : nullptr, a.V};
     const float T = a.temp[r];
@@ -121,7 +120,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_sample(FilterArgs a) {
 // The place of the draw at u among what the filters keep, the pick being the
 // n-th candidate there, and the kept mass.
 template <int NP, bool SPANS>
-__device__ __forceinline__ HistPlace draw(HistOrder<NP, SPANS> &order, int k, float p, float mp, float u, double &mass,
+__device__ __forceinline__ HistPlace draw(HistOrder<HistRow<NP, SPANS>> &order, int k, float p, float mp, float u, double &mass,
                                           uint32_t &n) {
     const int lane = threadIdx.x & 63;
     const uint32_t top = order.top_pos();
@@ -193,7 +192,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     const float mp = a.min_p ? a.min_p[r] : 0.f;
     const float u = a.uniform[r];
     const bool greedy = !(T > 0.f);
-    HistOrder<NP, SPANS> order(sh, row);
+    HistOrder<HistRow<NP, SPANS>> order(sh, row);
     if (!order.build(greedy ? 1.0 : 1.0 / (double)T)) {
         if (threadIdx.x == 0) {
             a.ids[r] = -1;
@@ -219,6 +218,51 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
         const double x = (double)bits_value(pos_bits(pos));
         const double y = x == order.weight.m ? 0.0 : (x - order.weight.m) * order.weight.inv_t;
         a.ids[r] = id;
+        a.logprob[r] = (float)(y - log_of(mass));
+    }
+}
+
+// float32 rows: the filters as ranks (row_fine.hpp).
+template <int NP, bool SPANS>
+__global__ __launch_bounds__(kRowThreads) void k_filter_fine(FilterArgs a) {
+    __shared__ HistShared sh;
+    __shared__ union {
+        FineShared fine;
+        SelectShared select;
+    } more;
+    FineShared &fs = more.fine;
+    const int r = blockIdx.x;
+    FineRow<NP, SPANS, false> row;
+    row.init((const float *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr, a.V);
+    const float T = a.temp[r];
+    const int k = a.top_k ? a.top_k[r] : 0;
+    const float p = a.top_p ? a.top_p[r] : 1.f;
+    const float mp = a.min_p ? a.min_p[r] : 0.f;
+    const float u = a.uniform[r];
+    const bool greedy = !(T > 0.f);
+    HistOrder<FineRow<NP, SPANS, false>> order(sh, row);
+    int i = -1;
+    double mass = 0.0;
+    if (order.build(greedy ? 1.0 : 1.0 / (double)T)) {
+        FineDraw<FineRow<NP, SPANS, false>> fine{order, fs};
+        i = fine.draw(greedy, k, p, mp, u, mass);
+    } else if (!order.overflowed) {
+        if (threadIdx.x == 0) {
+            a.ids[r] = -1;
+            a.logprob[r] = 0.f;
+        }
+        return;
+    }
+    if (i < 0) {
+        __syncthreads();
+        filter_by_digits<0>(a, r, more.select);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        const uint64_t e = fs.list[i];
+        const double x = (double)value_of_key(~(uint32_t)(e >> 32));
+        const double y = x == order.weight.m ? 0.0 : (x - order.weight.m) * order.weight.inv_t;
+        a.ids[r] = (int32_t)(uint32_t)e;
         a.logprob[r] = (float)(y - log_of(mass));
     }
 }
@@ -257,7 +301,7 @@ int cg_filter_sample(const void *d_logits, int32_t dtype, int32_t batch, int32_t
     const FilterArgs a{d_logits, row_stride, d_mask, words_per_row, vocab, d_temperature,
                        d_top_k,  d_top_p,    d_min_p, d_uniform,    d_out_ids, d_out_logprob};
     if (dtype == 0) {
-        hipLaunchKernelGGL((k_filter_sample<0>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
+        CG_LAUNCH_FINE(k_filter_fine, vocab, batch, (hipStream_t)stream, a);
     } else {
         CG_LAUNCH_ROWS(k_filter_counts, vocab, batch, (hipStream_t)stream, a);
     }

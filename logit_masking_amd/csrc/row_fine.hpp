@@ -1,0 +1,472 @@
+// row_fine.hpp -- the order of one masked row of float32 logits, by one
+// workgroup.
+//
+// The counts of row_hist.hpp by the logits' upper 16 bits place every rank
+// within a few candidates and every mass within the width of a bin.  What is
+// exact comes from a window: the candidates of a range of positions, at most
+// kWindow of them, gathered and sorted with the mass of everything above them
+// summed in the same pass, one exponential per logit that counts.  A rank's
+// bin is known from the counts; a mass is looked for around where the bins'
+// middle values put it, which is nearly always right, and else further on.
+// All comes out as ranks: top-k, top-p and min-p each keep the ranks below
+// some number.
+#pragma once
+#include "row_hist.hpp"
+
+namespace cg {
+
+constexpr int kFinePieceIds = 4 * kRowThreads;  // ids of one 16-byte load of every thread
+constexpr uint32_t kWindow = 1024;              // candidates of a window: one a thread
+constexpr uint32_t kNegInf = 0xFF800000u;
+constexpr uint32_t kLeastKey = 0x00800000u;  // of the type's lowest value
+
+// The row: NP pieces a thread in registers; with SPANS, longer rows in spans
+// of NP, read again by every pass.  SUM: each thread also keeps the maximum
+// of its candidates and the sum of e^(x - maximum), in float32.
+template <int NP, bool SPANS, bool SUM>
+struct FineRow {
+    static constexpr int kSpan = NP * kFinePieceIds;
+    static constexpr bool kExact = false;  // a position is a bin of 2^16 values
+    // A bin by its middle, no larger than the largest candidate.
+    static __device__ __forceinline__ float bin_value(uint32_t bits, float most) {
+        return bits == (uint32_t)kInfIdx ? INFINITY : fminf(__uint_as_float(bits << 16 | 0x8000u), most);
+    }
+    __amdgpu_buffer_rsrc_t rx, rm;
+    const float *x;
+    const uint64_t *mask;
+    int V, skew;
+    uint32_t d[NP][4];
+    float run_max = -INFINITY, run_sum = 0.f;
+
+    __device__ void init(const void *logits, const uint64_t *m, int vocab) {
+        x = (const float *)logits;
+        mask = m;
+        V = vocab;
+        skew = (int)(((uintptr_t)logits & 15) >> 2);
+        rx = __builtin_amdgcn_make_buffer_rsrc((void *)(x - skew), (short)0, (V + skew) * 4, kBufWord3);
+        rm = __builtin_amdgcn_make_buffer_rsrc((void *)m, (short)0, m ? (vocab + 63) / 64 * 8 : 0, kBufWord3);
+    }
+    __device__ int spans() const { return SPANS ? (V + skew + kSpan - 1) / kSpan : 1; }
+    __device__ int first_id(int span, int p) const {
+        return span * kSpan + p * kFinePieceIds + (int)threadIdx.x * 4 - skew;
+    }
+    __device__ __forceinline__ uint32_t usable(int span, int p, uint32_t raw) const {
+        const int f = first_id(span, p), left = V - f;
+        uint32_t b = (mask ? raw >> (f & 7) : raw) & 0xFu;
+        if (f < 0) b &= 0xFu << -f;
+        return left >= 4 ? b : left <= 0 ? 0u : b & ((1u << left) - 1u);
+    }
+    // Reads a span: what is no candidate (masked, -inf, NaN) as -inf, zeros as +0.
+    __device__ __forceinline__ void ask_mask(int span, uint32_t (&raw)[NP]) const {
+#pragma unroll
+        for (int p = 0; p < NP; p++) {
+            raw[p] = 0xFFFFu;
+            if (mask) {
+                const int at = first_id(span, p) >> 3;
+                raw[p] = __builtin_amdgcn_raw_buffer_load_b8(rm, at, 0, 0);
+                if (skew) raw[p] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rm, at + 1, 0, 0) << 8;
+            }
+        }
+    }
+    static constexpr int kWords = (NP + 7) / 8;
+    __device__ __forceinline__ void ask(int span, const uint32_t (&raw)[NP], uint32_t (&bits)[kWords]) {
+#pragma unroll
+        for (int p = 0; p < NP; p++) {
+            const uint32_t b = usable(span, p, raw[p]);
+            bits[p / 8] = (p % 8 ? bits[p / 8] : 0u) | b << (4 * (p % 8));
+            const uint4 v = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                          rx, b ? (first_id(span, p) + skew) * 4 : 0x7FFFFFF0, 0, 0));
+            d[p][0] = v.x; d[p][1] = v.y; d[p][2] = v.z; d[p][3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void select(int p, const uint32_t (&bits)[kWords]) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float v = __uint_as_float(d[p][j]) + 0.f;
+            d[p][j] = ((bits[p / 8] >> (4 * (p % 8) + j)) & 1) && v > -INFINITY ? __float_as_uint(v) : kNegInf;
+        }
+    }
+    __device__ __forceinline__ void load(int span) {
+        uint32_t raw[NP], bits[kWords];
+        ask_mask(span, raw);
+        ask(span, raw, bits);
+#pragma unroll
+        for (int p = 0; p < NP; p++) select(p, bits);
+    }
+    __device__ __forceinline__ void add(const float (&v)[4]) {
+        const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        constexpr float kLog2e = 1.4426950408889634f;
+        if (top > run_max) {
+            run_sum *= __builtin_amdgcn_exp2f((run_max - top) * kLog2e);
+            run_max = top;
+        }
+        const float base = run_max == -INFINITY ? 0.f : run_max;  // only -inf so far
+#pragma unroll
+        for (int j = 0; j < 4; j++) run_sum += __builtin_amdgcn_exp2f((v[j] - base) * kLog2e);
+    }
+
+    // Reads and counts the row and finds its largest key.
+    template <class F>
+    __device__ __forceinline__ void read_and_count(HistShared &sh, F while_waiting) {
+        char *h = (char *)sh.h;
+        const uint32_t none = (uint32_t)((char *)&sh.dummy[threadIdx.x & 63] - h);
+        float top = -INFINITY;
+        const int n_spans = spans();
+        for (int span = 0; span < n_spans; span++) {
+            uint32_t raw[NP], bits[kWords];
+            ask_mask(span, raw);
+            if (span == 0) while_waiting();
+            ask(span, raw, bits);
+            if (span == 0) __syncthreads();  // the counts are cleared
+#pragma unroll
+            for (int p = 0; p < NP; p++) {
+                select(p, bits);
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const uint32_t w = d[p][j];
+                    v[j] = __uint_as_float(w);
+                    atomicAdd((uint32_t *)(h + (w != kNegInf ? (w >> 14) & 0x1FFFCu : none)), (int)w < 0 ? 0x10000u : 1u);
+                }
+                top = fmaxf(fmaxf(top, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
+                if (SUM) add(v);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int s = 32; s; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+        if ((threadIdx.x & 63) == 0 && top > -INFINITY) atomicMax(&sh.top_key, key_of_bits(__float_as_uint(top)));
+    }
+    // f(key, id) for every element; what is no candidate has a key below every candidate's.
+    template <class F>
+    __device__ __forceinline__ void each(F f) {
+        const int n_spans = spans();
+        for (int span = 0; span < n_spans; span++) {
+            if (SPANS) load(span);
+            int first = first_id(span, 0);
+            asm volatile("" : "+v"(first));  // (nor from the ids)
+#pragma unroll
+            for (int p = 0; p < NP; p++) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    uint32_t w = d[p][j];
+                    asm volatile("" : "+v"(w));  // a caller's loop keeps nothing worked out from it
+                    f(key_of_bits(w), first + p * kFinePieceIds + j);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+};
+
+struct FineShared {
+    uint64_t list[kWindow];  // complement of the key, then the id: rising is the order
+    double mass[kWindow];    // inclusive sums over the list
+    double wave[kRowWaves];
+    double total;
+    uint32_t lo, hi, above;         // the window chosen: positions, candidates before it
+    double guess_above, guess_to;  // its bounds' mass by the bins
+    uint32_t n, key;
+    int hit;
+    bool crowded;
+};
+
+// Sorts list[0, n) rising; n <= kWindow, every thread calls it.  Steps within
+// 128 entries stay in one wave, whose LDS accesses keep their order.
+__device__ __forceinline__ void sort_rising(uint64_t *list, uint32_t n) {
+    uint32_t size_all = 2;
+    while (size_all < n) size_all <<= 1;
+    for (uint32_t i = n + threadIdx.x; i < size_all; i += kRowThreads) list[i] = ~0ull;
+    __syncthreads();
+    for (uint32_t size = 2; size <= size_all; size <<= 1) {
+        for (uint32_t step = size >> 1; step; step >>= 1) {
+            const uint32_t t = threadIdx.x;
+            if (t < size_all / 2) {
+                const uint32_t lo = 2 * t - (t & (step - 1)), hi = lo + step;
+                const uint64_t a = list[lo], b = list[hi];
+                if (((lo & size) == 0) == (a > b)) {
+                    list[lo] = b;
+                    list[hi] = a;
+                }
+            }
+            if (step > 64 || (step == 1 && size >= 128)) __syncthreads();
+            else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+    }
+    __syncthreads();
+}
+
+// The draw among the ranks that the filters keep.  One loop with one pass over
+// the row in it: each stage asks for a rank, a mass or a sum, which the window
+// answers if it holds the place, and a pass brings if not.
+template <class ROW>
+struct FineDraw {
+    HistOrder<ROW> &order;
+    FineShared &fs;
+
+    __device__ __forceinline__ double block_sum(double v) {
+        v = wave_scan(v);
+        if ((threadIdx.x & 63) == 63) fs.wave[threadIdx.x >> 6] = v;
+        __syncthreads();
+        double s = 0.0;
+#pragma unroll 1
+        for (int w = 0; w < kRowWaves; w++) s += fs.wave[w];
+        __syncthreads();
+        return s;
+    }
+
+    // Chooses a window that holds position q: from the top if that fits, else
+    // around it, with some ranks beyond if there is room.  Wave 0; the result
+    // goes to fs.
+    __device__ __forceinline__ void choose(const HistPlace &q, uint32_t beyond) {
+        const uint32_t end = q.above + q.count;
+        uint32_t a = 0, last = q.pos, before = 0;
+        bool fits = true;
+        if (end > kWindow) {
+            const HistPlace p = order.template find<0>(q.above > 128 ? q.above - 128 : 0, 0.0);
+            a = p.pos;
+            before = p.above;
+            if (end - before > kWindow) {
+                a = q.pos;
+                before = q.above;
+                fits = q.count <= kWindow;
+            }
+        }
+        if (fits && beyond) {
+            const HistPlace p = order.template find<0>(end - 1 + beyond, 0.0);
+            if (p.pos > last && p.above + p.count - before <= kWindow) last = p.pos;
+        }
+        const double m0 = a ? order.mass_to(a - 1) : 0.0, m1 = order.mass_to(last);
+        if (threadIdx.x == 0) {
+            fs.lo = a;
+            fs.hi = last;
+            fs.above = before;
+            fs.crowded = !fits;
+            fs.guess_above = m0;
+            fs.guess_to = m1;
+        }
+    }
+
+    // The least key whose weight is at least `least` (weights rise with the
+    // key): 64 points of the range at a time.  One wave.
+    __device__ __forceinline__ uint32_t least_key(double least) const {
+        uint32_t a = kLeastKey - 1, b = key_of_bits(__float_as_uint((float)order.weight.m));  // not at a, but at b
+        while (b - a > 1) {
+            const uint32_t step = (b - a + 63) / 64, at = min(a + ((threadIdx.x & 63) + 1) * step, b);
+            const int l = __builtin_ctzll(__ballot(order.weight(value_of_key(at)) >= least));  // lane 63 is at b
+            b = min(a + (uint32_t)(l + 1) * step, b);
+            a += (uint32_t)l * step;
+        }
+        return b;
+    }
+
+    // The list's index of the pick and the kept mass; -1 for a row that a
+    // window does not take.
+    __device__ __forceinline__ int draw(bool greedy, int k, float p, float mp, float u, double &mass) {
+        enum { kTopK, kTotal, kTopP, kMinP, kPick, kLast };      // stages
+        enum { kRank, kMore, kLeast, kSum };                     // what is asked for
+        const uint32_t t = threadIdx.x;
+        if (order.searches()) {
+            const uint32_t c = order.total_count();
+            const double m = order.total_mass();
+            if (t == 0) {
+                fs.n = c;
+                fs.total = m;
+            }
+        }
+        __syncthreads();
+        const uint32_t count = fs.n;
+        const double approx_total = fs.total;
+        __syncthreads();
+        // the window: positions lo .. hi hold the n listed candidates, `above` and mass_above lie before
+        uint32_t lo = 0, hi = 0, above = 0, n = 0;
+        double mass_above = 0.0, scale = 1.0;
+        uint32_t kept = count, key = kLeastKey, from = 0, to = 65535u;
+        double guess = -1.0;
+        mass = 0.0;
+        int tries = 0, stage = !greedy && k > 0 && (uint32_t)k < count ? kTopK : kTotal;
+        for (;;) {
+            const int ask = stage == kTopK || stage == kLast ? kRank : stage == kTopP ? kLeast : stage == kPick ? kMore : kSum;
+            const uint32_t rank = stage == kTopK ? (uint32_t)k - 1 : kept - 1;
+            const double target = stage == kTopP ? (double)p * mass : u > 0.f ? fmin((double)u, 1.0 - 0x1p-53) * mass : 0.0;
+            auto reached = [&](double m) { return ask == kLeast ? m >= target : m > target; };
+            bool have = false;
+            int i = 0;
+            uint32_t sum_ranks = 0;
+            double sum = 0.0;
+            // from the window
+            if (ask == kRank) {
+                have = n && above <= rank && rank < above + n;
+                i = (int)(rank - above);
+            } else if (ask == kSum) {
+                if (stage == kMinP && n) {
+                    if (kept <= above + n && key <= ~(uint32_t)(fs.list[kept > above ? kept - above - 1 : 0] >> 32) && kept > above) {
+                        have = true;  // the last kept weight reaches it: nothing goes
+                        sum_ranks = kept;
+                        sum = mass;
+                    } else if (lo == 0 && key > ~(uint32_t)(fs.list[n - 1] >> 32)) {
+                        // it ends within the list
+                        __syncthreads();
+                        if (t < n && ~(uint32_t)(fs.list[t] >> 32) >= key &&
+                            (t + 1 == n || ~(uint32_t)(fs.list[t + 1] >> 32) < key))
+                            fs.hit = (int)t;
+                        __syncthreads();
+                        have = true;
+                        sum_ranks = (uint32_t)fs.hit + 1;
+                        sum = fs.mass[fs.hit];
+                    }
+                }
+            } else if (n) {
+                const double end = mass_above + fs.mass[n - 1];
+                const bool before = lo > 0 && reached(mass_above), is_last = above + n >= count;
+                if (before) {
+                    to = min(to, lo - 1);
+                    guess = fs.guess_above * (target / mass_above);
+                } else if (!reached(end) && !is_last) {
+                    from = max(from, hi + 1);
+                    guess = fs.guess_to + (target - end) / scale;
+                } else {
+                    // the first that reaches it, else the last with weight
+                    __syncthreads();
+                    if (t == 0) fs.hit = 0;
+                    __syncthreads();
+                    if (t < n) {
+                        const double m1 = fs.mass[t], m0 = t ? fs.mass[t - 1] : 0.0;
+                        if (reached(end) ? reached(mass_above + m1) && (t == 0 || !reached(mass_above + m0))
+                                         : m1 > m0 && !(fs.mass[n - 1] > m1))
+                            fs.hit = (int)t;
+                    }
+                    __syncthreads();
+                    have = true;
+                    i = fs.hit;
+                }
+            }
+            // from the row
+            if (!have) {
+                if (++tries > 24) return -1;  // (the bounds of the search keep it far from this)
+                uint32_t key_hi = key - 1, key_lo = key;  // a sum: nothing is listed
+                if (ask != kSum) {
+                    if (guess < 0.0) guess = target / scale;
+                    __syncthreads();
+                    if (t < 64) {
+                        HistPlace q = ask == kRank    ? order.template find<0>(rank, 0.0)
+                                      : ask == kLeast ? order.template find<2>(0, guess)
+                                                      : order.template find<1>(0, guess);
+                        if (ask != kRank && (q.pos < from || q.pos > to)) {
+                            const uint32_t c = q.pos < from ? order.count_to(from - 1) : order.count_to(to) - 1;
+                            q = order.template find<0>(c, 0.0);
+                        }
+                        choose(q, ask == kRank ? 0 : 64 + (q.above + q.count) / 8);
+                        if (t == 0) fs.n = 0;
+                    }
+                    __syncthreads();
+                    if (fs.crowded) return -1;
+                    lo = fs.lo;
+                    hi = fs.hi;
+                    above = fs.above;
+                    key_hi = (65535u - lo) << 16 | 0xFFFFu;
+                    key_lo = (65535u - hi) << 16;
+                }
+                double s = 0.0;
+                uint32_t c = 0;
+                order.row.each([&](uint32_t v, int id) {
+                    if (v > key_hi) {
+                        s += order.weight(value_of_key(v));
+                        c++;
+                    } else if (v >= key_lo) {
+                        const uint32_t at = atomicAdd(&fs.n, 1u);
+                        if (at < kWindow) fs.list[at] = (uint64_t)~v << 32 | (uint32_t)id;
+                    }
+                });
+                s = block_sum(s);
+                if (ask == kSum) {
+                    have = true;
+                    sum = s;
+                    sum_ranks = (uint32_t)block_sum((double)c);
+                } else {
+                    mass_above = s;
+                    n = min(fs.n, kWindow);
+                    sort_rising(fs.list, n);
+                    const double w = t < n ? order.weight(value_of_key(~(uint32_t)(fs.list[t] >> 32))) : 0.0;
+                    const double m = wave_scan(w);
+                    if ((t & 63) == 63) fs.wave[t >> 6] = m;
+                    __syncthreads();
+                    double before = 0.0;
+#pragma unroll 1
+                    for (uint32_t v = 0; v < t >> 6; v++) before += fs.wave[v];
+                    fs.mass[t] = before + m;
+                    __syncthreads();
+                    continue;
+                }
+            }
+            // the stage's answer, and the next stage
+            const uint32_t end = above + (uint32_t)i + 1;
+            switch (stage) {
+                case kTopK:
+                    kept = (uint32_t)k;
+                    mass = mass_above + fs.mass[i];
+                    stage = kTopP;
+                    break;
+                case kTotal:
+                    mass = sum;
+                    scale = sum / approx_total;
+                    stage = greedy ? kLast : kTopP;
+                    if (greedy) kept = 1;
+                    break;
+                case kTopP:
+                    if (end < kept) {
+                        kept = end;
+                        mass = mass_above + fs.mass[i];
+                    }
+                    stage = kMinP;
+                    break;
+                case kMinP:
+                    if (sum_ranks < kept) {
+                        kept = sum_ranks;
+                        mass = sum;
+                    }
+                    stage = kPick;
+                    break;
+                case kPick:
+                    if (end <= kept) return i;
+                    stage = kLast;
+                    break;
+                default:
+                    return i;
+            }
+            if (stage == kTopP && !(p < 1.f)) stage = kMinP;
+            if (stage == kTopP && p <= 0.f) {
+                kept = 1;
+                mass = 1.0;
+                stage = kLast;
+            }
+            if (stage == kMinP && !(mp > 0.f)) stage = kPick;
+            if (stage == kMinP) {
+                if (t < 64) {
+                    const uint32_t v = least_key(fmin((double)mp, 1.0));
+                    if (t == 0) fs.key = v;
+                }
+                __syncthreads();
+                key = fs.key;
+            }
+            tries = 0;
+            from = 0;
+            to = 65535u;
+            guess = -1.0;
+        }
+    }
+};
+
+// Launches KERNEL<NP, SPANS> with as many pieces as rows of V ids need (3: the
+// largest skew); longer rows keep nothing between passes and are read in
+// spans of 8.
+#define CG_LAUNCH_FINE(KERNEL, V, BATCH, STREAM, ARGS)                                              \
+    do {                                                                                            \
+        const int pieces_ = ((V) + 3 + kFinePieceIds - 1) / kFinePieceIds;                          \
+        const dim3 grid_(BATCH), block_(kRowThreads);                                               \
+        if (pieces_ <= 8) hipLaunchKernelGGL((KERNEL<8, false>), grid_, block_, 0, STREAM, ARGS);   \
+        else if (pieces_ <= 16) hipLaunchKernelGGL((KERNEL<16, false>), grid_, block_, 0, STREAM, ARGS); \
+        else hipLaunchKernelGGL((KERNEL<8, true>), grid_, block_, 0, STREAM, ARGS);                 \
+    } while (0)
+
+}  // namespace cg

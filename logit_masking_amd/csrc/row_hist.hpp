@@ -44,6 +44,7 @@ struct HistShared {
     double blk_mass[kHistBlocks];
     uint32_t counted;    // sum of every count, the dummies' included
     uint32_t top_block;  // first block with a candidate
+    uint32_t top_key;    // key of the largest candidate (rows of float32)
     uint32_t n_blocks;   // blocks with a candidate, listed in any order
     uint16_t blocks[kHistBlocks];
     uint32_t list[kRowThreads];
@@ -100,6 +101,8 @@ __device__ __forceinline__ float bits_value(uint32_t b) { return __uint_as_float
 template <int NP, bool SPANS>
 struct HistRow {
     static constexpr int kSpan = NP * kPieceIds;
+    static constexpr bool kExact = true;  // a position is one value
+    static __device__ __forceinline__ float bin_value(uint32_t bits, float) { return bits_value(bits); }
     __amdgpu_buffer_rsrc_t rx, rm;
     const uint16_t *x;
     const uint64_t *mask;
@@ -445,10 +448,11 @@ __device__ __forceinline__ void bins(const HistShared &sh, int wide, int b, uint
 }
 // Weights of those positions; 1 where there is no candidate (a value above
 // the largest one may weigh inf).
+template <class ROW>
 __device__ __forceinline__ void bin_weights(const Weight &weight, int b, const uint32_t (&c)[4], double (&w)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; j++)
-        w[j] = weight(c[j] ? bits_value(pos_bits(b * 256 + 4 * (threadIdx.x & 63) + j)) : (float)weight.m);
+        w[j] = weight(c[j] ? ROW::bin_value(pos_bits(b * 256 + 4 * (threadIdx.x & 63) + j), (float)weight.m) : (float)weight.m);
 }
 
 // Lists the blocks that hold candidates and notes the first; where asked,
@@ -500,6 +504,7 @@ __device__ __forceinline__ void survey(HistShared &sh, int wide, bool sum_up) {
 }
 
 // Totals of the listed blocks, a block a wave.
+template <class ROW>
 __device__ __forceinline__ void total(HistShared &sh, int wide, const Weight &weight) {
     const int wave = threadIdx.x >> 6, n = (int)sh.n_blocks;
     for (int e = wave; e < n; e += kRowWaves) {
@@ -507,7 +512,7 @@ __device__ __forceinline__ void total(HistShared &sh, int wide, const Weight &we
         uint32_t c[4];
         double w[4];
         bins(sh, wide, b, c);
-        bin_weights(weight, b, c, w);
+        bin_weights<ROW>(weight, b, c, w);
         const double m = wave_scan(((double)c[0] * w[0] + (double)c[1] * w[1]) + ((double)c[2] * w[2] + (double)c[3] * w[3]));
         const int s = wave_scan((int)(c[0] + c[1] + c[2] + c[3]));
         if ((threadIdx.x & 63) == 63) {
@@ -544,6 +549,7 @@ __device__ __forceinline__ void recount(HistShared &sh, const uint16_t *x, const
 // The totals of a row one of whose counts overflowed; the positives first, so
 // that the largest candidate is known before its weights are needed.  Returns
 // its position; the negatives' counts stay in h.
+template <class ROW>
 __device__ __forceinline__ uint32_t total_wide(HistShared &sh, const uint16_t *x, const uint64_t *mask, int V, double inv_t) {
     __syncthreads();
     if (threadIdx.x == 0) sh.top_block = 0xFFFFFFFFu;
@@ -556,7 +562,7 @@ __device__ __forceinline__ uint32_t total_wide(HistShared &sh, const uint16_t *x
         survey(sh, sign, false);
         __syncthreads();
         if (top == 0xFFFFFFFFu && sh.top_block != 0xFFFFFFFFu) top = top_position(sh, sign);
-        total(sh, sign, Weight{(double)bits_value(pos_bits(top)), inv_t});
+        total<ROW>(sh, sign, Weight{(double)bits_value(pos_bits(top)), inv_t});
     }
     return top;
 }
@@ -565,11 +571,12 @@ __device__ __forceinline__ uint32_t total_wide(HistShared &sh, const uint16_t *x
 // (a workgroup's worth of waves running them alike costs their instructions
 // sixteen times: 5 us of 35 at 256 rows of 128256).  Only in a row counted
 // one sign at a time do all waves run them, since a search may count again.
-template <int NP, bool SPANS>
+template <class ROW>
 struct HistOrder {
     HistShared &sh;
-    HistRow<NP, SPANS> &row;
+    ROW &row;
     Weight weight;
+    bool overflowed;  // (rows of another type than bfloat16: nothing else is known then)
     int wide;  // -1: h holds both signs in 16 bits; 0 / 1: that sign in 32 bits
     // Candidates and mass up to the end of the lane's blocks 4 lane + j.
     uint32_t incl;
@@ -582,10 +589,10 @@ struct HistOrder {
         for (int j = 0; j < 4; j++) bm[j] = sh.blk_mass[4 * lane + j];
     }
 
-    __device__ __forceinline__ HistOrder(HistShared &s, HistRow<NP, SPANS> &r) : sh(s), row(r) {}
+    __device__ __forceinline__ HistOrder(HistShared &s, ROW &r) : sh(s), row(r) {}
 
     // Reads, counts and orders the row under weights 1 / T.  False: no candidate.
-    __device__ bool build(double inv_t) {
+    __device__ __forceinline__ bool build(double inv_t) {
         const int t = threadIdx.x;
         wide = -1;
         row.read_and_count(sh, [&] {
@@ -606,23 +613,30 @@ struct HistOrder {
                 sh.counted = 0;
                 sh.n_blocks = 0;
                 sh.top_block = 0xFFFFFFFFu;
+                sh.top_key = 0;
             }
         });
         __syncthreads();
         const bool check = row.V > 65535;  // a count may have overflowed
         survey(sh, -1, check);
         __syncthreads();
-        if (check && sh.counted != (uint32_t)row.spans() * (uint32_t)HistRow<NP, SPANS>::kSpan) {
-            top_pos_ = total_wide(sh, row.x, row.mask, row.V, inv_t);
+        overflowed = check && sh.counted != (uint32_t)row.spans() * (uint32_t)ROW::kSpan;
+        if constexpr (ROW::kExact) {
+            if (overflowed) {
+                top_pos_ = total_wide<ROW>(sh, row.x, row.mask, row.V, inv_t);
+                wide = 1;
+            } else if (sh.top_block != 0xFFFFFFFFu) {
+                top_pos_ = top_position(sh, -1);
+            } else {
+                return false;
+            }
             if (top_pos_ == 0xFFFFFFFFu) return false;
-            wide = 1;
             weight = Weight{(double)bits_value(pos_bits(top_pos_)), inv_t};
         } else {
-            if (sh.top_block == 0xFFFFFFFFu) return false;
-            top_pos_ = top_position(sh, -1);
-            weight = Weight{(double)bits_value(pos_bits(top_pos_)), inv_t};
-            total(sh, -1, weight);
+            if (sh.top_block == 0xFFFFFFFFu || overflowed) return false;
+            weight = Weight{(double)value_of_key(sh.top_key), inv_t};
         }
+        if (wide < 0) total<ROW>(sh, -1, weight);
         __syncthreads();
         if (searches()) {
             uint32_t bc[4];
@@ -678,7 +692,7 @@ struct HistOrder {
 
     // The place of the first position up to whose end ... (see pick).
     template <int HOW>
-    __device__ HistPlace find(uint32_t rank, double mass) {
+    __device__ __forceinline__ HistPlace find(uint32_t rank, double mass) {
         HistPlace q;
         q.above = 0;
         q.mass_above = 0.0;
@@ -688,7 +702,7 @@ struct HistOrder {
         const int b = pick<HOW>(c, m, incl, mass_incl, rank, mass, q.above, q.mass_above);
         hold(b);
         bins(sh, wide, b, c);
-        bin_weights(weight, b, c, w);
+        bin_weights<ROW>(weight, b, c, w);
 #pragma unroll
         for (int j = 0; j < 4; j++) m[j] = (double)c[j] * w[j];
         const uint32_t ci = (uint32_t)wave_scan((int)(c[0] + c[1] + c[2] + c[3]));
@@ -701,8 +715,23 @@ struct HistOrder {
         return q;
     }
 
+    // Candidates of the positions up to pos, its own included.
+    __device__ __forceinline__ uint32_t count_to(uint32_t pos) {
+        const int b = pos >> 8, lane = threadIdx.x & 63, at = (int)(pos & 255u);
+        uint32_t before = (uint32_t)from_left((int)incl), n = 0, c[4];
+        double m[4];
+        blocks(c, m);
+#pragma unroll
+        for (int j = 0; j < 3; j++) before += j < (b & 3) ? c[j] : 0u;
+        before = (uint32_t)lane_int((int)before, b >> 2);
+        hold(b);
+        bins(sh, wide, b, c);
+#pragma unroll
+        for (int j = 0; j < 4; j++) n += 4 * lane + j <= at ? c[j] : 0u;
+        return before + (uint32_t)lane_int(wave_scan((int)n), 63);
+    }
     // Mass of the positions up to pos, its own included.
-    __device__ double mass_to(uint32_t pos) {
+    __device__ __forceinline__ double mass_to(uint32_t pos) {
         const int b = pos >> 8, lane = threadIdx.x & 63, at = (int)(pos & 255u);
         double before = from_left(mass_incl), m = 0.0, w[4];
         uint32_t c[4];
@@ -712,7 +741,7 @@ struct HistOrder {
         before = lane_double(before, b >> 2);
         hold(b);
         bins(sh, wide, b, c);
-        bin_weights(weight, b, c, w);
+        bin_weights<ROW>(weight, b, c, w);
 #pragma unroll
         for (int j = 0; j < 4; j++) m += 4 * lane + j <= at ? (double)c[j] * w[j] : 0.0;
         return before + lane_double(wave_scan(m), 63);
@@ -723,9 +752,11 @@ struct HistOrder {
 
     // Block b's counts in h (a row counted one sign at a time holds one).
     __device__ __forceinline__ void hold(int b) {
-        if (wide >= 0 && wide != (b >= kHistBlocks / 2)) {  // uniform
-            wide = b >= kHistBlocks / 2;
-            recount(sh, row.x, row.mask, row.V, wide);
+        if constexpr (ROW::kExact) {
+            if (wide >= 0 && wide != (b >= kHistBlocks / 2)) {  // uniform
+                wide = b >= kHistBlocks / 2;
+                recount(sh, row.x, row.mask, row.V, wide);
+            }
         }
     }
 };

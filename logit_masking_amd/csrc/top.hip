@@ -6,8 +6,7 @@
 #include <algorithm>
 
 #include "cg_internal.hpp"
-#include "row_hist.hpp"
-#include "row_select.hpp"
+#include "row_fine.hpp"
 
 namespace cg {
 
@@ -41,18 +40,24 @@ __device__ void sort_falling(uint64_t *list, int n) {
     __syncthreads();
 }
 
+// The whole row digit by digit (row_select.hpp), for float32 rows with more
+// candidates in the k-th one's bin than the list takes.
+struct DigitsShared {
+    SelectShared select;
+    uint64_t list[CG_MAX_TOP];  // key in the high half, the id's complement in the low: one order
+    uint32_t n_list;
+};
 template <int DT>
-__global__ __launch_bounds__(kRowThreads) void k_top_logits(TopArgs a) {
-    __shared__ SelectShared sh;
-    __shared__ uint64_t list[CG_MAX_TOP];  // key in the high half, the id's complement in the low: one order
-    __shared__ uint32_t n_list;
-    const int r = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__device__ void top_by_digits(const TopArgs &a, int r, DigitsShared &ds) {
+    SelectShared &sh = ds.select;
+    uint64_t *list = ds.list;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     RowView<DT> row{(const char *)a.logits + (size_t)r * (size_t)a.stride * (DT == 0 ? 4 : 2),
                     a.mask ? a.mask + (size_t)r * a.wpr : nullptr, a.V};
     int n_pow = 1;
     while (n_pow < a.k) n_pow <<= 1;
     for (int i = threadIdx.x; i < n_pow; i += kRowThreads) list[i] = 0;
-    if (threadIdx.x == 0) n_list = 0;
+    if (threadIdx.x == 0) ds.n_list = 0;
     const uint32_t best = row_max_key(row, sh);
     uint64_t mass = 0;
     if (best) {
@@ -65,7 +70,7 @@ __global__ __launch_bounds__(kRowThreads) void k_top_logits(TopArgs a) {
         for (int base = 0; base < row.V; base += kRowThreads) {
             const int i = base + threadIdx.x;
             const uint32_t key = i < row.V ? row.key(i) : 0u;
-            if (key > q.key) list[atomicAdd(&n_list, 1u)] = ((uint64_t)key << 32) | (uint32_t)~i;
+            if (key > q.key) list[atomicAdd(&ds.n_list, 1u)] = ((uint64_t)key << 32) | (uint32_t)~i;
             const uint64_t hits = __ballot(key == q.key);
             if (lane == 0) sh.wave[wave] = __popcll(hits);
             __syncthreads();
@@ -140,7 +145,7 @@ __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
     HistRow<NP, SPANS> row;
     row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
              a.wpr, a.V);
-    HistOrder<NP, SPANS> order(sh, row);
+    HistOrder<HistRow<NP, SPANS>> order(sh, row);
     uint64_t *list = (uint64_t *)sh.h;
     uint32_t n = 0;
     if (order.build(1.0)) {
@@ -177,6 +182,60 @@ __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
     write_top(list, n, a, r, [](uint32_t pos) { return bits_value(pos_bits(pos)); });
 }
 
+// float32 rows: the k-th one's bin from the counts (row_fine.hpp), then the
+// candidates down to its end.
+template <int NP, bool SPANS>
+__global__ __launch_bounds__(kRowThreads) void k_top_fine(TopArgs a) {
+    __shared__ HistShared sh;
+    __shared__ union {
+        double sum[kRowWaves];
+        DigitsShared digits;
+    } more;
+    const int r = blockIdx.x;
+    FineRow<NP, SPANS, true> row;
+    row.init((const float *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr, a.V);
+    HistOrder<FineRow<NP, SPANS, true>> order(sh, row);
+    uint64_t *list = (uint64_t *)sh.h;
+    uint32_t n = 0;
+    if (order.build(1.0)) {
+        const double part = row.run_sum ? (double)row.run_sum * exp_falling((double)row.run_max - order.weight.m) : 0.0;
+        const double whole = wave_scan(part);
+        if ((threadIdx.x & 63) == 63) more.sum[threadIdx.x >> 6] = whole;
+        if (order.searches()) {
+            const HistPlace q = order.template find<0>((uint32_t)a.k - 1, 0.0);
+            if (threadIdx.x == 0) {
+                sh.place = q;
+                sh.n_list = 0;
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            double s = 0.0;
+            for (int w = 0; w < kRowWaves; w++) s += more.sum[w];
+            a.lse[r] = (float)(order.weight.m < INFINITY ? order.weight.m + log_of(s) : INFINITY);
+        }
+        const HistPlace q = sh.place;
+        n = q.above + q.count;
+        if (n > kListRoom) {
+            __syncthreads();
+            top_by_digits<0>(a, r, more.digits);
+            return;
+        }
+        const uint32_t key_lo = (65535u - q.pos) << 16;
+        row.each([&](uint32_t key, int id) {
+            if (key >= key_lo) list[atomicAdd(&sh.n_list, 1u)] = (uint64_t)~key << 32 | (uint32_t)id;
+        });
+    } else if (order.overflowed) {
+        __syncthreads();
+        top_by_digits<0>(a, r, more.digits);
+        return;
+    } else if (threadIdx.x == 0) {
+        a.lse[r] = -INFINITY;
+    }
+    __syncthreads();
+    write_top(list, n, a, r, [](uint32_t key) { return value_of_key(~key); });
+}
+
 }  // namespace
 
 }  // namespace cg
@@ -209,10 +268,11 @@ int cg_top_logits(const void *d_logits, int32_t dtype, int32_t batch, int32_t vo
     if (!d_logits || !d_out_ids || !d_out_logits || !d_out_lse) return top_arg_error("NULL device pointer");
     (void)d_workspace;
     const TopArgs a{d_logits, row_stride, d_mask, words_per_row, vocab, k, d_out_ids, d_out_logits, d_out_lse};
-    if (dtype == 0)
-        hipLaunchKernelGGL((k_top_logits<0>), dim3(batch), dim3(kRowThreads), 0, (hipStream_t)stream, a);
-    else
+    if (dtype == 0) {
+        CG_LAUNCH_FINE(k_top_fine, vocab, batch, (hipStream_t)stream, a);
+    } else {
         CG_LAUNCH_ROWS(k_top_counts, vocab, batch, (hipStream_t)stream, a);
+    }
     return launch_status("top_logits");
 }
 
