@@ -515,13 +515,14 @@ def _row_lib():
 def _rows(logits, mask, vocab):
     """(dtype code, rows, vocab, row stride, mask address, words) of the logits and mask of a row operator."""
     import torch
-    if logits.dtype is torch.bfloat16:
+    dtype = logits.dtype
+    if dtype is torch.bfloat16:
         dt = DTYPE_BF16
-    elif logits.dtype is torch.float32:
+    elif dtype is torch.float32:
         dt = DTYPE_F32
     else:
         raise ValueError("logits must be float32 or bfloat16")
-    if logits.device.type != "cuda" or logits.dim() != 2 or logits.stride(1) != 1:
+    if not logits.is_cuda or logits.dim() != 2 or logits.stride(1) != 1:
         raise ValueError("logits must be a 2-D device tensor with unit column stride")
     B, cols = logits.shape
     V = cols if vocab is None else vocab
@@ -529,31 +530,36 @@ def _rows(logits, mask, vocab):
         raise ValueError("vocab out of range of the logits' columns")
     if V > MAX_ROW_VOCAB:
         raise ValueError(f"vocab above {MAX_ROW_VOCAB}")
-    # a row of its own may have any stride
-    stride = max(logits.stride(0), V) if B == 1 else logits.stride(0)
+    stride = logits.stride(0)
     if stride < V:
-        raise ValueError("logits' rows overlap")
+        if B > 1:
+            raise ValueError("logits' rows overlap")
+        stride = V  # a row of its own may have any stride
     if mask is None:
         return dt, B, V, stride, None, 0
-    _row_arg(mask, torch.int64, "mask", logits, (B, None))
+    _row_arg(mask, torch.int64, "mask", logits.get_device(), B, None)
     if mask.shape[1] < (V + 63) // 64:
         raise ValueError("mask has fewer than ceil(vocab / 64) words per row")
     return dt, B, V, stride, mask.data_ptr(), mask.shape[1]
 
 
-def _row_arg(t, dtype, name, logits, shape):
-    """A contiguous tensor beside the logits with at least shape[0] rows (and exactly shape[1] columns); its address."""
+def _row_arg(t, dtype, name, device, rows, cols=0):
+    """The address of a contiguous tensor on device number `device` with at
+    least `rows` rows: 1-D for cols = 0, else 2-D with `cols` columns (None:
+    any number)."""
+    shape = t.shape
+    if (t.dtype is dtype and t.get_device() == device and t.is_contiguous() and shape[0] >= rows and
+            (len(shape) == 1 if cols == 0 else len(shape) == 2 and (cols is None or shape[1] == cols))):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != logits.device:
+    if t.get_device() != device:
         raise ValueError(f"{name} must be on the logits' device")
-    if t.dim() != len(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {len(shape)} dims")
-    if t.shape[0] < shape[0]:
+    if t.dim() != (1 if cols == 0 else 2) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {1 if cols == 0 else 2} dims")
+    if shape[0] < rows:
         raise ValueError(f"{name} has fewer rows than logits")
-    if len(shape) > 1 and shape[1] is not None and t.shape[1] != shape[1]:
-        raise ValueError(f"{name} must have {shape[1]} columns")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have {cols} columns")
 
 
 def _workspace_arg(t, need, logits):
@@ -561,24 +567,24 @@ def _workspace_arg(t, need, logits):
         if need:
             raise ValueError("a workspace is needed")
         return None
-    if t.device != logits.device or not t.is_contiguous():
+    if t.get_device() != logits.get_device() or not t.is_contiguous():
         raise ValueError("workspace must be contiguous on the logits' device")
     if t.numel() * t.element_size() < need:
         raise ValueError("workspace too small")
     return t.data_ptr()
 
 
-def _row_call(fn, logits, stream, *args):
-    """fn(*args, stream) on the logits' device."""
+def _row_call(fn, device, stream, *args):
+    """fn(*args, stream) on device number `device`."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(logits.device)
-    raw = getattr(stream, "cuda_stream", stream) or 0
-    if logits.device.index != torch.cuda.current_device():
-        with torch.cuda.device(logits.device):
-            rc = fn(*args, raw)
-    else:
+        stream = torch.cuda.current_stream(device)
+    raw = getattr(stream, "cuda_stream", stream) or None
+    if device == torch.cuda.current_device():
         rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, raw)
     if rc != CG_OK:
         _check(rc)
 
@@ -604,15 +610,15 @@ def filter_sample(logits, mask, temperature, top_k, top_p, min_p, uniform, works
     import torch
     L = _row_lib()
     dt, B, V, stride, m, words = _rows(logits, mask, vocab)
-    f32, i32, n = torch.float32, torch.int32, (B,)
-    _row_call(L.cg_filter_sample, logits, stream, logits.data_ptr(), dt, B, V, stride, m, words,
-              _row_arg(temperature, f32, "temperature", logits, n),
-              None if top_k is None else _row_arg(top_k, i32, "top_k", logits, n),
-              None if top_p is None else _row_arg(top_p, f32, "top_p", logits, n),
-              None if min_p is None else _row_arg(min_p, f32, "min_p", logits, n),
-              _row_arg(uniform, f32, "uniform", logits, n),
+    f32, i32, dev = torch.float32, torch.int32, logits.get_device()
+    _row_call(L.cg_filter_sample, dev, stream, logits.data_ptr(), dt, B, V, stride, m, words,
+              _row_arg(temperature, f32, "temperature", dev, B),
+              None if top_k is None else _row_arg(top_k, i32, "top_k", dev, B),
+              None if top_p is None else _row_arg(top_p, f32, "top_p", dev, B),
+              None if min_p is None else _row_arg(min_p, f32, "min_p", dev, B),
+              _row_arg(uniform, f32, "uniform", dev, B),
               _workspace_arg(workspace, L.cg_filter_workspace_bytes(B, V), logits),
-              _row_arg(out_ids, i32, "out_ids", logits, n), _row_arg(out_logprob, f32, "out_logprob", logits, n))
+              _row_arg(out_ids, i32, "out_ids", dev, B), _row_arg(out_logprob, f32, "out_logprob", dev, B))
 
 
 def top_workspace_bytes(B: int, V: int, k: int) -> int:
@@ -635,12 +641,12 @@ def top_logits(logits, mask, workspace, out_ids, out_logits, out_lse, vocab=None
     dt, B, V, stride, m, words = _rows(logits, mask, vocab)
     if out_ids.dim() != 2:
         raise ValueError("out_ids must be [B, k]")
-    k = out_ids.shape[1]
-    _row_call(L.cg_top_logits, logits, stream, logits.data_ptr(), dt, B, V, stride, m, words, k,
+    k, dev = out_ids.shape[1], logits.get_device()
+    _row_call(L.cg_top_logits, dev, stream, logits.data_ptr(), dt, B, V, stride, m, words, k,
               _workspace_arg(workspace, L.cg_top_workspace_bytes(B, V, k), logits),
-              _row_arg(out_ids, torch.int32, "out_ids", logits, (B, k)),
-              _row_arg(out_logits, torch.float32, "out_logits", logits, (B, k)),
-              _row_arg(out_lse, torch.float32, "out_lse", logits, (B,)))
+              _row_arg(out_ids, torch.int32, "out_ids", dev, B, k),
+              _row_arg(out_logits, torch.float32, "out_logits", dev, B, k),
+              _row_arg(out_lse, torch.float32, "out_lse", dev, B))
 
 
 def _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab):
@@ -648,15 +654,15 @@ def _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
     dt, B, V, stride, m, words = _rows(logits, mask, vocab)
     if teacher_ids.dim() != 2:
         raise ValueError("teacher_ids must be [rows, k]")
-    k = teacher_ids.shape[1]
-    return B, V, (logits.data_ptr(), dt, B, V, stride, m, words,
-                  _row_arg(teacher_ids, torch.int32, "teacher_ids", logits, (B, k)),
-                  _row_arg(teacher_logits, torch.float32, "teacher_logits", logits, (B, k)), k, temperature)
+    k, dev = teacher_ids.shape[1], logits.get_device()
+    return dev, B, V, (logits.data_ptr(), dt, B, V, stride, m, words,
+                       _row_arg(teacher_ids, torch.int32, "teacher_ids", dev, B, k),
+                       _row_arg(teacher_logits, torch.float32, "teacher_logits", dev, B, k), k, temperature)
 
 
 def _grad_arg(grad, logits, B, V):
     """(address, row stride) of a gradient: the logits themselves, or rows apart from them."""
-    if grad.dtype is not logits.dtype or grad.device != logits.device:
+    if grad.dtype is not logits.dtype or grad.get_device() != logits.get_device():
         raise ValueError("out_grad must have the logits' dtype and device")
     if grad.dim() != 2 or grad.stride(1) != 1 or grad.shape[0] < B or grad.shape[1] < V:
         raise ValueError("out_grad must be [rows, >= vocab] with unit column stride")
@@ -681,14 +687,14 @@ def distill_topk(logits, mask, teacher_ids, teacher_logits, temperature, out_los
     in out_grad [rows, >= vocab] of the logits' dtype (it may be `logits`)."""
     import torch
     L = _row_lib()
-    B, V, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
+    dev, B, V, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
     f32 = torch.float32
     if (weight is None) != (out_grad is None):
         raise ValueError("weight and out_grad go together")
     g, gs = (None, 0) if out_grad is None else _grad_arg(out_grad, logits, B, V)
-    _row_call(L.cg_distill_topk, logits, stream, *args, _row_arg(out_loss, f32, "out_loss", logits, (B,)),
-              None if out_lse is None else _row_arg(out_lse, f32, "out_lse", logits, (B,)),
-              None if weight is None else _row_arg(weight, f32, "weight", logits, (B,)), g, gs)
+    _row_call(L.cg_distill_topk, dev, stream, *args, _row_arg(out_loss, f32, "out_loss", dev, B),
+              None if out_lse is None else _row_arg(out_lse, f32, "out_lse", dev, B),
+              None if weight is None else _row_arg(weight, f32, "weight", dev, B), g, gs)
 
 
 def distill_topk_grad(logits, mask, teacher_ids, teacher_logits, temperature, lse, weight, out_grad, vocab=None,
@@ -696,10 +702,10 @@ def distill_topk_grad(logits, mask, teacher_ids, teacher_logits, temperature, ls
     """cg_distill_topk_grad: distill_topk's gradient alone, from the lse it wrote."""
     import torch
     L = _row_lib()
-    B, V, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
+    dev, B, V, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
     g, gs = _grad_arg(out_grad, logits, B, V)
-    _row_call(L.cg_distill_topk_grad, logits, stream, *args, _row_arg(lse, torch.float32, "lse", logits, (B,)),
-              _row_arg(weight, torch.float32, "weight", logits, (B,)), g, gs)
+    _row_call(L.cg_distill_topk_grad, dev, stream, *args, _row_arg(lse, torch.float32, "lse", dev, B),
+              _row_arg(weight, torch.float32, "weight", dev, B), g, gs)
 
 
 _distill_fn = None

@@ -47,7 +47,7 @@ __device__ void filter_by_digits(const FilterArgs &a, int r, SelectShared &sh) {
         }
         return;
     }
-    const Weight weight{(double)value_of_key(best), greedy ? 1.0 : 1.0 / (double)T};
+    const Weight weight(value_of_key(best), greedy ? 1.0 : 1.0 / (double)T);
     const int k = a.top_k ? a.top_k[r] : 0;
     const float p = a.top_p ? a.top_p[r] : 1.f;
     const float mp = a.min_p ? a.min_p[r] : 0.f;
@@ -110,8 +110,7 @@ __device__ void filter_by_digits(const FilterArgs &a, int r, SelectShared &sh) {
     }
     const int id = row_nth(row, pick_key, pick_n, sh);
     if (threadIdx.x == 0) {
-        const float x = value_of_key(pick_key);
-        const double y = (double)x == weight.m ? 0.0 : ((double)x - weight.m) * weight.inv_t;
+        const double y = weight.exponent(value_of_key(pick_key));
         a.ids[r] = id;
         a.logprob[r] = (float)(y - log_of((double)mass / kMassUnit));
     }
@@ -193,7 +192,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     const float u = a.uniform[r];
     const bool greedy = !(T > 0.f);
     HistOrder<HistRow<NP, SPANS>> order(sh, row);
-    if (!order.build(greedy ? 1.0 : 1.0 / (double)T)) {
+    if (!order.template build<true>(greedy ? 1.0 : 1.0 / (double)T)) {
         if (threadIdx.x == 0) {
             a.ids[r] = -1;
             a.logprob[r] = 0.f;
@@ -215,8 +214,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     const double mass = sh.mass;
     const int id = row.nth(pos, count, n, sh);
     if (threadIdx.x == 0) {
-        const double x = (double)bits_value(pos_bits(pos));
-        const double y = x == order.weight.m ? 0.0 : (x - order.weight.m) * order.weight.inv_t;
+        const double y = order.weight.exponent(bits_value(pos_bits(pos)));
         a.ids[r] = id;
         a.logprob[r] = (float)(y - log_of(mass));
     }
@@ -243,7 +241,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_fine(FilterArgs a) {
     HistOrder<FineRow<NP, SPANS, false>> order(sh, row);
     int i = -1;
     double mass = 0.0;
-    if (order.build(greedy ? 1.0 : 1.0 / (double)T)) {
+    if (order.template build<false>(greedy ? 1.0 : 1.0 / (double)T)) {
         FineDraw<FineRow<NP, SPANS, false>> fine{order, fs};
         i = fine.draw(greedy, k, p, mp, u, mass);
     } else if (!order.overflowed) {
@@ -260,8 +258,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_fine(FilterArgs a) {
     }
     if (threadIdx.x == 0) {
         const uint64_t e = fs.list[i];
-        const double x = (double)value_of_key(~(uint32_t)(e >> 32));
-        const double y = x == order.weight.m ? 0.0 : (x - order.weight.m) * order.weight.inv_t;
+        const double y = order.weight.exponent(value_of_key(~(uint32_t)(e >> 32)));
         a.ids[r] = (int32_t)(uint32_t)e;
         a.logprob[r] = (float)(y - log_of(mass));
     }

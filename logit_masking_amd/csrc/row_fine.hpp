@@ -137,21 +137,21 @@ struct FineRow {
         for (int s = 32; s; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
         if ((threadIdx.x & 63) == 0 && top > -INFINITY) atomicMax(&sh.top_key, key_of_bits(__float_as_uint(top)));
     }
-    // f(key, id) for every element; what is no candidate has a key below every candidate's.
+    // f(x, id) for every element; what is no candidate is -inf.
     template <class F>
     __device__ __forceinline__ void each(F f) {
         const int n_spans = spans();
         for (int span = 0; span < n_spans; span++) {
             if (SPANS) load(span);
             int first = first_id(span, 0);
-            asm volatile("" : "+v"(first));  // (nor from the ids)
+            asm volatile("" : "+v"(first));  // a caller's loop keeps nothing worked out from the ids
 #pragma unroll
             for (int p = 0; p < NP; p++) {
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     uint32_t w = d[p][j];
-                    asm volatile("" : "+v"(w));  // a caller's loop keeps nothing worked out from it
-                    f(key_of_bits(w), first + p * kFinePieceIds + j);
+                    asm volatile("" : "+v"(w));  // (nor from the logits)
+                    f(__uint_as_float(w), first + p * kFinePieceIds + j);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -159,16 +159,30 @@ struct FineRow {
     }
 };
 
+// The smallest and the largest value of a bin.  Position 32767 is both zeros'
+// and holds what is nearer to them than a bin's width, on both sides; the
+// infinite one's bounds are infinite.
+__device__ __forceinline__ float bin_low(uint32_t pos) {
+    return pos == 32767u ? value_of_key(0x7FFF0000u) : pos < 128u ? INFINITY : value_of_key((65535u - pos) << 16);
+}
+__device__ __forceinline__ float bin_high(uint32_t pos) {
+    return pos < 128u ? INFINITY : value_of_key((65535u - pos) << 16 | 0xFFFFu);
+}
+// The position of a key.
+__device__ __forceinline__ uint32_t key_pos(uint32_t key) {
+    const uint32_t pos = 65535u - (key >> 16);
+    return pos == 32768u ? 32767u : pos;
+}
+
 struct FineShared {
     uint64_t list[kWindow];  // complement of the key, then the id: rising is the order
     double mass[kWindow];    // inclusive sums over the list
     double wave[kRowWaves];
-    double total;
-    uint32_t lo, hi, above;         // the window chosen: positions, candidates before it
-    double guess_above, guess_to;  // its bounds' mass by the bins
-    uint32_t n, key;
+    uint32_t lo, hi, above;  // the window chosen: positions, candidates before it
+    uint32_t n, key, before, end;
+    double value[2];
     int hit;
-    bool crowded;
+    bool fits;
 };
 
 // Sorts list[0, n) rising; n <= kWindow, every thread calls it.  Steps within
@@ -197,8 +211,9 @@ __device__ __forceinline__ void sort_rising(uint64_t *list, uint32_t n) {
 }
 
 // The draw among the ranks that the filters keep.  One loop with one pass over
-// the row in it: each stage asks for a rank, a mass or a sum, which the window
-// answers if it holds the place, and a pass brings if not.
+// the row in it: each stage asks for a rank, a mass, the end of the weights
+// from some value on, or the whole mass, which the window answers if it holds
+// the place, and a pass brings if not.
 template <class ROW>
 struct FineDraw {
     HistOrder<ROW> &order;
@@ -208,49 +223,100 @@ struct FineDraw {
         v = wave_scan(v);
         if ((threadIdx.x & 63) == 63) fs.wave[threadIdx.x >> 6] = v;
         __syncthreads();
-        double s = 0.0;
-#pragma unroll 1
-        for (int w = 0; w < kRowWaves; w++) s += fs.wave[w];
+        v = fs.wave[threadIdx.x & (kRowWaves - 1)];
+        v += __shfl_xor(v, 1);
+        v += __shfl_xor(v, 2);
+        v += __shfl_xor(v, 4);
+        v += __shfl_xor(v, 8);
         __syncthreads();
-        return s;
+        return v;
     }
 
-    // Chooses a window that holds position q: from the top if that fits, else
-    // around it, with some ranks beyond if there is room.  Wave 0; the result
-    // goes to fs.
-    __device__ __forceinline__ void choose(const HistPlace &q, uint32_t beyond) {
-        const uint32_t end = q.above + q.count;
-        uint32_t a = 0, last = q.pos, before = 0;
-        bool fits = true;
+    // Sorts the list by the bins' own counts: each entry goes to its bin's
+    // stretch, then to its place among the few there.  Windows of more bins
+    // than fit, or with many candidates in one bin, take the general sort (55
+    // steps for 1024 entries: 9 us).
+    __device__ __forceinline__ void sort_window(uint32_t lo, uint32_t hi, uint32_t n) {
+        constexpr uint32_t kBins = sizeof(fs.mass) / 4;  // two a thread
+        if (hi - lo >= kBins || n > kRowThreads) {
+            sort_rising(fs.list, n);
+            return;
+        }
+        uint32_t *const end = (uint32_t *)fs.mass;
+        const uint32_t t = threadIdx.x;
+        __syncthreads();
+        const uint64_t e = t < n ? fs.list[t] : 0;
+        uint32_t c[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint32_t pos = lo + 2 * t + i;
+            c[i] = pos <= hi ? bin_count(pos) : 0u;
+        }
+        const uint32_t sum = (uint32_t)wave_scan((int)(c[0] + c[1]));
+        constexpr uint32_t kCrowd = 0x80000000u;
+        const uint32_t crowd = __any(c[0] > 192 || c[1] > 192) ? kCrowd : 0u;
+        if ((t & 63) == 63) order.sh.w_cnt[t >> 6] = sum | crowd;
+        __syncthreads();
+        uint32_t before = (t & 63) < kRowWaves ? order.sh.w_cnt[t & 15] : 0u;
+        if (__any((before & kCrowd) != 0)) {  // alike in every wave
+            sort_rising(fs.list, n);
+            return;
+        }
+        before = (uint32_t)lane_int(wave_scan((t & 63) < (t >> 6) ? (int)before : 0), 63);
+        const uint32_t start = before + sum - c[0] - c[1];
+        end[2 * t] = start;
+        end[2 * t + 1] = start + c[0];
+        __syncthreads();
+        const uint32_t bin = t < n ? key_pos(~(uint32_t)(e >> 32)) - lo : 0u;
+        if (t < n) fs.list[atomicAdd(&end[bin], 1u)] = e;
+        __syncthreads();
+        uint32_t at = 0;
+        if (t < n) {
+            at = bin ? end[bin - 1] : 0u;
+#pragma unroll 4
+            for (uint32_t i = at, last = end[bin]; i < last; i++) at += fs.list[i] < e;
+        }
+        __syncthreads();
+        if (t < n) fs.list[at] = e;
+        __syncthreads();
+    }
+    // Candidates of one position.
+    __device__ __forceinline__ uint32_t bin_count(uint32_t pos) const {
+        const uint32_t i = pos_bits(pos) & 0x7FFFu;
+        uint32_t cp, cn;
+        cleaned(-1, (int)i, order.sh.h[i], cp, cn);
+        return pos < 32768u ? cp : cn;
+    }
+
+    // Chooses a window of whole bins that holds the ranks from `start` up to
+    // `end` (a bin's end): from the top if that fits, else around them; with
+    // `beyond` ranks more if there is room.  Wave 0; the result goes to fs.
+    __device__ __forceinline__ void choose(uint32_t start, uint32_t end, uint32_t last, uint32_t beyond) {
+        uint32_t a = key_pos(order.sh.top_key), before = 0;
         if (end > kWindow) {
-            const HistPlace p = order.template find<0>(q.above > 128 ? q.above - 128 : 0, 0.0);
+            HistPlace p = order.find_rank(start > 128 ? start - 128 : 0);
+            if (end - p.above > kWindow) p = order.find_rank(start);
             a = p.pos;
             before = p.above;
-            if (end - before > kWindow) {
-                a = q.pos;
-                before = q.above;
-                fits = q.count <= kWindow;
-            }
         }
+        const bool fits = end - before <= kWindow;
         if (fits && beyond) {
-            const HistPlace p = order.template find<0>(end - 1 + beyond, 0.0);
+            const HistPlace p = order.find_rank(end - 1 + beyond);
             if (p.pos > last && p.above + p.count - before <= kWindow) last = p.pos;
         }
-        const double m0 = a ? order.mass_to(a - 1) : 0.0, m1 = order.mass_to(last);
         if (threadIdx.x == 0) {
             fs.lo = a;
             fs.hi = last;
             fs.above = before;
-            fs.crowded = !fits;
-            fs.guess_above = m0;
-            fs.guess_to = m1;
+            fs.fits = fits;
+            fs.n = 0;
         }
     }
 
     // The least key whose weight is at least `least` (weights rise with the
     // key): 64 points of the range at a time.  One wave.
     __device__ __forceinline__ uint32_t least_key(double least) const {
-        uint32_t a = kLeastKey - 1, b = key_of_bits(__float_as_uint((float)order.weight.m));  // not at a, but at b
+        uint32_t a = kLeastKey - 1, b = key_of_bits(__float_as_uint(order.weight.largest()));  // not at a, but at b
         while (b - a > 1) {
             const uint32_t step = (b - a + 63) / 64, at = min(a + ((threadIdx.x & 63) + 1) * step, b);
             const int l = __builtin_ctzll(__ballot(order.weight(value_of_key(at)) >= least));  // lane 63 is at b
@@ -263,68 +329,83 @@ struct FineDraw {
     // The list's index of the pick and the kept mass; -1 for a row that a
     // window does not take.
     __device__ __forceinline__ int draw(bool greedy, int k, float p, float mp, float u, double &mass) {
-        enum { kTopK, kTotal, kTopP, kMinP, kPick, kLast };      // stages
-        enum { kRank, kMore, kLeast, kSum };                     // what is asked for
+        enum { kTopK, kMinP, kTotal, kTopP, kPick, kLast };  // stages
         const uint32_t t = threadIdx.x;
         if (order.searches()) {
             const uint32_t c = order.total_count();
-            const double m = order.total_mass();
-            if (t == 0) {
-                fs.n = c;
-                fs.total = m;
-            }
+            if (t == 0) fs.n = c;
         }
         __syncthreads();
         const uint32_t count = fs.n;
-        const double approx_total = fs.total;
         __syncthreads();
         // the window: positions lo .. hi hold the n listed candidates, `above` and mass_above lie before
         uint32_t lo = 0, hi = 0, above = 0, n = 0;
-        double mass_above = 0.0, scale = 1.0;
-        uint32_t kept = count, key = kLeastKey, from = 0, to = 65535u;
-        double guess = -1.0;
-        mass = 0.0;
-        int tries = 0, stage = !greedy && k > 0 && (uint32_t)k < count ? kTopK : kTotal;
+        double mass_above = 0.0;
+        // the ranks kept so far and their mass (< 0: not known yet), and what top-p is a share of
+        uint32_t kept = count;
+        double base = -1.0, scale = 1.0, guess = -1.0;
+        mass = -1.0;
+        uint32_t from = 0, to = 65535u, key = 0, c_before = 0, c_end = 0;
+        bool masses = false, valued = false, whole = false;  // the bins have theirs; the window's bounds too; base is all
+        int tries = 0, stage = greedy ? kTotal : k > 0 && (uint32_t)k < count ? kTopK : kMinP;
+        if (!greedy && p <= 0.f) {
+            kept = 1;
+            mass = 1.0;
+            stage = kLast;
+        }
         for (;;) {
-            const int ask = stage == kTopK || stage == kLast ? kRank : stage == kTopP ? kLeast : stage == kPick ? kMore : kSum;
+            if (stage == kMinP && key == 0) {
+                if (!(mp > 0.f)) {
+                    stage = kTotal;
+                } else {
+                    if (t < 64) {
+                        const uint32_t v = least_key(fmin((double)mp, 1.0)), pos = key_pos(v);
+                        const uint32_t e = order.count_to(pos), b = pos ? order.count_to(pos - 1) : 0u;
+                        if (t == 0) {
+                            fs.key = v;
+                            fs.before = b;
+                            fs.end = e;
+                        }
+                    }
+                    __syncthreads();
+                    key = fs.key;
+                    c_before = fs.before;
+                    c_end = fs.end;
+                    if (c_before >= kept) stage = kTotal;  // it keeps them all
+                }
+            }
+            if (stage == kTotal && (greedy ? false : base >= 0.0 || (mass >= 0.0 && !(p < 1.f)))) stage = kTopP;
+            if (stage == kTopP && (!(p < 1.f) || mass < (double)p * base)) stage = kPick;
+            if (stage == kLast && kept == 0) return -1;
+            const bool by_mass = stage == kTopP || stage == kPick;
             const uint32_t rank = stage == kTopK ? (uint32_t)k - 1 : kept - 1;
-            const double target = stage == kTopP ? (double)p * mass : u > 0.f ? fmin((double)u, 1.0 - 0x1p-53) * mass : 0.0;
-            auto reached = [&](double m) { return ask == kLeast ? m >= target : m > target; };
+            const double target = stage == kTopP ? (double)p * base : u > 0.f ? fmin((double)u, 1.0 - 0x1p-53) * mass : 0.0;
+            auto reached = [&](double m) { return stage == kTopP ? m >= target : m > target; };
             bool have = false;
             int i = 0;
-            uint32_t sum_ranks = 0;
-            double sum = 0.0;
             // from the window
-            if (ask == kRank) {
+            if (stage == kTopK || stage == kLast) {
                 have = n && above <= rank && rank < above + n;
                 i = (int)(rank - above);
-            } else if (ask == kSum) {
-                if (stage == kMinP && n) {
-                    if (kept <= above + n && key <= ~(uint32_t)(fs.list[kept > above ? kept - above - 1 : 0] >> 32) && kept > above) {
-                        have = true;  // the last kept weight reaches it: nothing goes
-                        sum_ranks = kept;
-                        sum = mass;
-                    } else if (lo == 0 && key > ~(uint32_t)(fs.list[n - 1] >> 32)) {
-                        // it ends within the list
-                        __syncthreads();
-                        if (t < n && ~(uint32_t)(fs.list[t] >> 32) >= key &&
-                            (t + 1 == n || ~(uint32_t)(fs.list[t + 1] >> 32) < key))
-                            fs.hit = (int)t;
-                        __syncthreads();
-                        have = true;
-                        sum_ranks = (uint32_t)fs.hit + 1;
-                        sum = fs.mass[fs.hit];
-                    }
+            } else if (stage == kMinP) {
+                if (n && (above == 0 || above < c_before) && c_end <= above + n) {
+                    __syncthreads();
+                    if (t == 0) fs.hit = 0;
+                    __syncthreads();
+                    if (t < n && ~(uint32_t)(fs.list[t] >> 32) >= key && (t + 1 == n || ~(uint32_t)(fs.list[t + 1] >> 32) < key))
+                        fs.hit = (int)t;
+                    __syncthreads();
+                    have = true;
+                    i = fs.hit;
                 }
-            } else if (n) {
+            } else if (by_mass && n) {
                 const double end = mass_above + fs.mass[n - 1];
-                const bool before = lo > 0 && reached(mass_above), is_last = above + n >= count;
-                if (before) {
+                if (lo > 0 && reached(mass_above)) {
                     to = min(to, lo - 1);
-                    guess = fs.guess_above * (target / mass_above);
-                } else if (!reached(end) && !is_last) {
+                    guess = valued ? fs.value[0] * (target / mass_above) : target / scale;
+                } else if (!reached(end) && above + n < count) {
                     from = max(from, hi + 1);
-                    guess = fs.guess_to + (target - end) / scale;
+                    guess = valued ? fs.value[1] + (target - end) / scale : target / scale;
                 } else {
                     // the first that reaches it, else the last with weight
                     __syncthreads();
@@ -344,110 +425,105 @@ struct FineDraw {
             // from the row
             if (!have) {
                 if (++tries > 24) return -1;  // (the bounds of the search keep it far from this)
-                uint32_t key_hi = key - 1, key_lo = key;  // a sum: nothing is listed
-                if (ask != kSum) {
-                    if (guess < 0.0) guess = target / scale;
+                float x_hi = -INFINITY, x_lo = INFINITY;  // the whole mass: nothing is listed
+                if (by_mass && !masses) {
+                    order.add_masses();
+                    masses = true;
+                    if (whole) {
+                        if (order.searches()) {
+                            const double m = order.total_mass();
+                            if (t == 0) fs.value[0] = m;
+                        }
+                        __syncthreads();
+                        scale = base / fs.value[0];
+                        __syncthreads();
+                    }
+                }
+                if (stage != kTotal) {
+                    if (!(guess >= 0.0)) guess = target / scale;
                     __syncthreads();
                     if (t < 64) {
-                        HistPlace q = ask == kRank    ? order.template find<0>(rank, 0.0)
-                                      : ask == kLeast ? order.template find<2>(0, guess)
-                                                      : order.template find<1>(0, guess);
-                        if (ask != kRank && (q.pos < from || q.pos > to)) {
-                            const uint32_t c = q.pos < from ? order.count_to(from - 1) : order.count_to(to) - 1;
-                            q = order.template find<0>(c, 0.0);
+                        if (stage == kMinP) {
+                            const HistPlace q = order.find_rank(c_end > c_before ? c_end - 1 : c_before - 1);
+                            choose(c_before ? c_before - 1 : 0, q.above + q.count, q.pos, 0);
+                        } else {
+                            HistPlace q;
+                            if (by_mass) {
+                                q = stage == kTopP ? order.template find<2>(0, guess) : order.template find<1>(0, guess);
+                                if (q.pos < from) q = order.find_rank(order.count_to(from - 1));
+                                else if (q.pos > to) q = order.find_rank(order.count_to(to) - 1);
+                            } else {
+                                q = order.find_rank(rank);
+                            }
+                            choose(q.above, q.above + q.count, q.pos, by_mass ? 64 + (q.above + q.count) / 8 : 0);
                         }
-                        choose(q, ask == kRank ? 0 : 64 + (q.above + q.count) / 8);
-                        if (t == 0) fs.n = 0;
                     }
                     __syncthreads();
-                    if (fs.crowded) return -1;
+                    if (!fs.fits) return -1;
                     lo = fs.lo;
                     hi = fs.hi;
                     above = fs.above;
-                    key_hi = (65535u - lo) << 16 | 0xFFFFu;
-                    key_lo = (65535u - hi) << 16;
+                    x_hi = bin_high(lo);
+                    x_lo = bin_low(hi);
                 }
                 double s = 0.0;
-                uint32_t c = 0;
-                order.row.each([&](uint32_t v, int id) {
-                    if (v > key_hi) {
-                        s += order.weight(value_of_key(v));
-                        c++;
-                    } else if (v >= key_lo) {
+                order.row.each([&](float x, int id) {
+                    if (x > x_hi) {
+                        s += order.weight(x);
+                    } else if (x >= x_lo) {
                         const uint32_t at = atomicAdd(&fs.n, 1u);
-                        if (at < kWindow) fs.list[at] = (uint64_t)~v << 32 | (uint32_t)id;
+                        if (at < kWindow) fs.list[at] = (uint64_t)~key_of_bits(__float_as_uint(x)) << 32 | (uint32_t)id;
                     }
                 });
                 s = block_sum(s);
-                if (ask == kSum) {
-                    have = true;
-                    sum = s;
-                    sum_ranks = (uint32_t)block_sum((double)c);
-                } else {
-                    mass_above = s;
-                    n = min(fs.n, kWindow);
-                    sort_rising(fs.list, n);
-                    const double w = t < n ? order.weight(value_of_key(~(uint32_t)(fs.list[t] >> 32))) : 0.0;
-                    const double m = wave_scan(w);
-                    if ((t & 63) == 63) fs.wave[t >> 6] = m;
-                    __syncthreads();
-                    double before = 0.0;
-#pragma unroll 1
-                    for (uint32_t v = 0; v < t >> 6; v++) before += fs.wave[v];
-                    fs.mass[t] = before + m;
-                    __syncthreads();
+                if (stage == kTotal) {
+                    base = s;
+                    whole = true;
+                    if (mass < 0.0) mass = s;
+                    if (greedy) kept = 1;
+                    stage = greedy ? kLast : kTopP;
+                    tries = 0;
                     continue;
                 }
+                mass_above = s;
+                n = min(fs.n, kWindow);
+                sort_window(lo, hi, n);
+                const double w = t < n ? order.weight(value_of_key(~(uint32_t)(fs.list[t] >> 32))) : 0.0;
+                const double m = wave_scan(w);
+                if ((t & 63) == 63) fs.wave[t >> 6] = m;
+                __syncthreads();
+                double before = 0.0;
+#pragma unroll 1
+                for (uint32_t v = 0; v < t >> 6; v++) before += fs.wave[v];
+                fs.mass[t] = before + m;
+                valued = by_mass;
+                if (by_mass && t < 64) {  // the bounds' mass by the bins, for another try
+                    const double m0 = lo ? order.mass_to(lo - 1) : 0.0, m1 = order.mass_to(hi);
+                    if (t == 0) {
+                        fs.value[0] = m0;
+                        fs.value[1] = m1;
+                    }
+                }
+                __syncthreads();
+                continue;
             }
             // the stage's answer, and the next stage
             const uint32_t end = above + (uint32_t)i + 1;
-            switch (stage) {
-                case kTopK:
-                    kept = (uint32_t)k;
-                    mass = mass_above + fs.mass[i];
-                    stage = kTopP;
-                    break;
-                case kTotal:
-                    mass = sum;
-                    scale = sum / approx_total;
-                    stage = greedy ? kLast : kTopP;
-                    if (greedy) kept = 1;
-                    break;
-                case kTopP:
-                    if (end < kept) {
-                        kept = end;
-                        mass = mass_above + fs.mass[i];
-                    }
-                    stage = kMinP;
-                    break;
-                case kMinP:
-                    if (sum_ranks < kept) {
-                        kept = sum_ranks;
-                        mass = sum;
-                    }
-                    stage = kPick;
-                    break;
-                case kPick:
-                    if (end <= kept) return i;
-                    stage = kLast;
-                    break;
-                default:
-                    return i;
-            }
-            if (stage == kTopP && !(p < 1.f)) stage = kMinP;
-            if (stage == kTopP && p <= 0.f) {
-                kept = 1;
-                mass = 1.0;
-                stage = kLast;
-            }
-            if (stage == kMinP && !(mp > 0.f)) stage = kPick;
-            if (stage == kMinP) {
-                if (t < 64) {
-                    const uint32_t v = least_key(fmin((double)mp, 1.0));
-                    if (t == 0) fs.key = v;
+            const double m_end = mass_above + fs.mass[i];
+            if (stage == kTopK) {
+                kept = (uint32_t)k;
+                base = mass = m_end;
+                stage = kMinP;
+            } else if (stage == kMinP || stage == kTopP) {
+                if (end < kept) {
+                    kept = end;
+                    mass = m_end;
                 }
-                __syncthreads();
-                key = fs.key;
+                stage = stage == kMinP ? kTotal : kPick;
+            } else if (stage == kPick && end > kept) {
+                stage = kLast;
+            } else {
+                return i;
             }
             tries = 0;
             from = 0;

@@ -89,6 +89,12 @@ __device__ __forceinline__ double lane_double(double v, int l) {
     return __longlong_as_double(((long long)hi << 32) | (unsigned)lo);
 }
 
+// sum + the two 16-bit halves of c
+__device__ __forceinline__ uint32_t add_halves(uint32_t c, uint32_t sum) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_udot2(__builtin_bit_cast(u16x2, c), (u16x2){1, 1}, sum, false);
+}
+
 __device__ __forceinline__ uint32_t pos_bits(uint32_t pos) {
     return pos < 32768u ? 32767u - pos : pos;  // negatives: 0x8000 | magnitude
 }
@@ -294,10 +300,9 @@ struct HistRow {
         }
     }
 
-    // Calls take(rank, id) for the first `upto` candidates of position pos by
-    // rising id, reading the row again 1024 ids at a time.
-    template <class F>
-    __device__ void walk(uint32_t pos, uint32_t upto, HistShared &sh, F take) const {
+    // Lists the first `upto` candidates of position pos by rising id, reading
+    // the row again 1024 ids at a time (more of one value than the list takes).
+    __device__ void first_of(uint32_t pos, uint32_t upto, uint64_t *list, HistShared &sh) const {
         const uint32_t bits = pos_bits(pos), same = bits == 0 ? 0x7FFFu : 0xFFFFu;  // the two zeros
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         uint32_t before = 0;
@@ -315,104 +320,119 @@ struct HistRow {
                 before += c;
             }
             mine += __popcll(hits & ((1ull << lane) - 1));
-            if (hit && mine < upto) take(mine, i);
+            if (hit && mine < upto) list[mine] = (uint64_t)pos << 32 | (uint32_t)i;
             __syncthreads();
         }
     }
-    // The first `upto` candidates of position pos, listed in order.
-    __device__ void first_of(uint32_t pos, uint32_t upto, uint64_t *list, HistShared &sh) const {
-        walk(pos, upto, sh, [&](uint32_t rank, int id) { list[rank] = ((uint64_t)pos << 32) | (uint32_t)id; });
-    }
-
-    // Lists the ids of the registers' candidates of one value, any order.
-    __device__ __forceinline__ void matches(uint32_t want, uint32_t same, uint32_t *list, HistShared &sh) {
-        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-        for (int p = 0; p < NP; p++) {
-            if (!((live >> p) & 1)) continue;
-            const uint32_t y0 = (d[p][0] ^ want) & same, y1 = (d[p][1] ^ want) & same;
-            const uint32_t y2 = (d[p][2] ^ want) & same, y3 = (d[p][3] ^ want) & same;
-            u16x2 m = __builtin_elementwise_min(__builtin_bit_cast(u16x2, y0), __builtin_bit_cast(u16x2, y1));
-            m = __builtin_elementwise_min(
-                m, __builtin_elementwise_min(__builtin_bit_cast(u16x2, y2), __builtin_bit_cast(u16x2, y3)));
-            if (m.x == 0 || m.y == 0) {
-                uint32_t at = ((y0 & 0xFFFFu) ? 0u : 1u) | ((y0 >> 16) ? 0u : 2u) | ((y1 & 0xFFFFu) ? 0u : 4u) |
-                              ((y1 >> 16) ? 0u : 8u) | ((y2 & 0xFFFFu) ? 0u : 16u) | ((y2 >> 16) ? 0u : 32u) |
-                              ((y3 & 0xFFFFu) ? 0u : 64u) | ((y3 >> 16) ? 0u : 128u);
-                do {  // nearly always one
-                    list[atomicAdd(&sh.n_list, 1u)] = first_id(span_at, p) + __builtin_ctz(at);
-                    at &= at - 1;
-                } while (at);
-            }
+    // Whether the two halves of each of a piece's words are the value.
+    struct Match {
+        uint32_t want, same;  // the value's bits twice; what of them counts (the two zeros)
+        __device__ __forceinline__ explicit Match(uint32_t pos) {
+            const uint32_t bits = pos_bits(pos);
+            want = bits | bits << 16;
+            same = bits == 0 ? 0x7FFF7FFFu : 0xFFFFFFFFu;
         }
-    }
+        __device__ __forceinline__ uint32_t rest(uint32_t w) const { return (w ^ want) & same; }
+        static __device__ __forceinline__ bool low(uint32_t rest) { return (uint16_t)rest == 0; }
+        static __device__ __forceinline__ bool high(uint32_t rest) { return rest < 0x10000u; }
+        // Bit j: id j of a piece is the value.
+        static __device__ __forceinline__ uint32_t bits(uint32_t y0, uint32_t y1, uint32_t y2, uint32_t y3) {
+            return (low(y0) ? 1u : 0u) | (high(y0) ? 2u : 0u) | (low(y1) ? 4u : 0u) | (high(y1) ? 8u : 0u) |
+                   (low(y2) ? 16u : 0u) | (high(y2) ? 32u : 0u) | (low(y3) ? 64u : 0u) | (high(y3) ? 128u : 0u);
+        }
+    };
 
     // The id of the n-th (from 0) of the row's `count` candidates of position
-    // pos, by rising id.
-    __device__ int nth(uint32_t pos, uint32_t count, uint32_t n, HistShared &sh) {
-        const uint32_t bits = pos_bits(pos);
-        const uint32_t same = bits == 0 ? 0x7FFF7FFFu : 0xFFFFFFFFu;  // the two zeros
-        const uint32_t want = bits | (bits << 16);
-        uint32_t *list = sh.list;
-        if (count > kRowThreads) {
-            // many: walk the row again
-            if (threadIdx.x == 0) sh.found = -1;
-            walk(pos, n + 1, sh, [&](uint32_t rank, int id) {
-                if (rank == n) sh.found = id;
-            });
-            return sh.found;
-        }
-        // few: list them; the n-th is the one with n smaller ones.  A longer
-        // row's last span is in the registers: its ids are the largest, the
-        // other spans are read again only if the n-th is not among them.
-        auto clear = [&] {
-            __syncthreads();
-            if (threadIdx.x == 0) sh.n_list = 0;
-            list[threadIdx.x] = 0xFFFFFFFFu;
-            __syncthreads();
-        };
-        clear();
-        matches(want, same, list, sh);
-        __syncthreads();
-        uint32_t listed = sh.n_list;
-        const int n_spans = spans();
-        if (n_spans > 1) {
-            const uint32_t before = count - listed;
-            if (n >= before) {
-                n -= before;
-            } else {
-                clear();
-                listed = 0;
-                for (int s = 0; s + 1 < n_spans && listed <= n; s++) {  // uniform
-                    load(s, sh.lut);
-                    matches(want, same, list, sh);
-                    __syncthreads();
-                    listed = sh.n_list;
-                    __syncthreads();
+    // pos, by rising id: counted by piece and wave, which is the ids' order,
+    // then the one wave that holds it looks closer.  A longer row's last span
+    // is in the registers: its ids are the largest, the other spans are read
+    // again only if the n-th is not among them.
+    __device__ __forceinline__ int nth(uint32_t pos, uint32_t count, uint32_t n, HistShared &sh) {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        const Match match(pos);
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_spans = spans();
+        uint32_t *const cnt = sh.list;  // by piece, then wave
+        static_assert(NP * kRowWaves <= kRowThreads, "the counts fit");
+        uint32_t before = 0;  // in the spans looked at
+        for (int s = 0; s < n_spans; s++) {
+            if (SPANS && s) load(s - 1, sh.lut);
+            // ids of a piece that differ, two pieces a register, then summed over the wave
+            uint32_t other[(NP + 1) / 2];
+#pragma unroll
+            for (int p = 0; p < NP; p++) {
+                uint32_t o = 8;
+                if ((live >> p) & 1) {
+                    u16x2 m = (u16x2){0, 0};
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        m += __builtin_elementwise_min(__builtin_bit_cast(u16x2, match.rest(d[p][j])), (u16x2){1, 1});
+                    o = add_halves(__builtin_bit_cast(uint32_t, m), 0);
                 }
+                other[p / 2] = p % 2 ? other[p / 2] | o << 16 : o;
+                __builtin_amdgcn_sched_barrier(0);
             }
-        }
-        if (threadIdx.x < listed) {
-            const uint32_t id = list[threadIdx.x];
-            const uint4 *four = (const uint4 *)list;
-            uint32_t smaller = 0;
-#pragma unroll 4
-            for (uint32_t i = 0; i < (listed + 3) / 4; i++) {
-                const uint4 v = four[i];
-                smaller += (v.x < id) + (v.y < id) + (v.z < id) + (v.w < id);
+#pragma unroll
+            for (int i = 0; i < (NP + 1) / 2; i++) other[i] = (uint32_t)wave_scan((int)other[i]);  // the last lane has the sum
+            __syncthreads();  // (the counts' last readers)
+            if (lane == 63) {
+#pragma unroll
+                for (int p = 0; p < NP; p++) cnt[p * kRowWaves + wave] = 512u - ((other[p / 2] >> (16 * (p % 2))) & 0xFFFFu);
             }
-            if (smaller == n) sh.found = (int)id;
+            __syncthreads();
+            // every wave: where the n-th is
+            constexpr int kEach = (NP * kRowWaves + 63) / 64;
+            uint32_t c[kEach], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; i++) {
+                c[i] = lane * kEach + i < NP * kRowWaves ? cnt[lane * kEach + i] : 0u;
+                sum += c[i];
+            }
+            const uint32_t incl = (uint32_t)wave_scan((int)sum);
+            const uint32_t all = (uint32_t)lane_int((int)incl, 63);
+            uint32_t skip = before;
+            if (SPANS && s == 0 && n_spans > 1) {  // the last span
+                skip = count - all;
+                if (n < skip) continue;
+            }
+            if (n < skip + all) {
+                const uint32_t left = n - skip;
+                const int L = __builtin_ctzll(__ballot(incl > left));
+                uint32_t at = 0, first = incl - sum, run = first;
+                bool done = false;
+#pragma unroll
+                for (int i = 0; i < kEach; i++) {
+                    const bool is = !done && run + c[i] > left;
+                    at = is ? (uint32_t)(lane * kEach + i) : at;
+                    first = is ? run : first;
+                    done = done || is;
+                    run += c[i];
+                }
+                const int where = lane_int((int)at, L);
+                uint32_t rest = left - (uint32_t)lane_int((int)first, L);
+                if (where % kRowWaves == wave) {
+                    const int piece = where / kRowWaves;
+                    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int p = 0; p < NP; p++)
+                        if (p == piece) {  // uniform
+#pragma unroll
+                            for (int j = 0; j < 4; j++) w[j] = match.rest(d[p][j]);
+                        }
+                    uint32_t bits = match.bits(w[0], w[1], w[2], w[3]);
+                    const uint32_t mine = __popc(bits), upto = (uint32_t)wave_scan((int)mine);
+                    if (upto > rest && upto - mine <= rest) {
+                        for (uint32_t i = rest - (upto - mine); i; i--) bits &= bits - 1;
+                        sh.found = first_id(span_at, piece) + __builtin_ctz(bits);
+                    }
+                }
+                break;
+            }
+            before += all;
         }
         __syncthreads();
         return sh.found;
     }
 };
-
-// sum + the two 16-bit halves of c
-__device__ __forceinline__ uint32_t add_halves(uint32_t c, uint32_t sum) {
-    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-    return __builtin_amdgcn_udot2(__builtin_bit_cast(u16x2, c), (u16x2){1, 1}, sum, false);
-}
 
 __device__ __forceinline__ void clear_counts(HistShared &sh) {
     uint4 *h = (uint4 *)sh.h;
@@ -446,13 +466,31 @@ __device__ __forceinline__ void bins(const HistShared &sh, int wide, int b, uint
         c[j] = neg ? cn : cp;
     }
 }
-// Weights of those positions; 1 where there is no candidate (a value above
-// the largest one may weigh inf).
+// Weights of those positions; what stands where there is no candidate is
+// finite and of no meaning.  Four positions of bfloat16 values in a row are
+// equally far apart, so their weights are a geometric progression: two
+// exponentials, while a step is small (the first may lie three steps above
+// the largest candidate) and none of them is infinite.
 template <class ROW>
 __device__ __forceinline__ void bin_weights(const Weight &weight, int b, const uint32_t (&c)[4], double (&w)[4]) {
+    const uint32_t pos = b * 256 + 4 * (threadIdx.x & 63);
+    if constexpr (ROW::kExact) {
+        const double y0 = weight.exponent(bits_value(pos_bits(pos))), y1 = weight.exponent(bits_value(pos_bits(pos + 1)));
+        const double step = y1 - y0;
+        if (b > 0 && b < kHistBlocks - 1 && __all(step >= -1.0 && step <= 0.0)) {
+            const double ratio = exp_falling(step);
+            w[0] = exp_falling(fmin(y0, 3.0));
+            w[1] = w[0] * ratio;
+            w[2] = w[1] * ratio;
+            w[3] = w[2] * ratio;
+            return;
+        }
+    }
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-        w[j] = weight(c[j] ? ROW::bin_value(pos_bits(b * 256 + 4 * (threadIdx.x & 63) + j), (float)weight.m) : (float)weight.m);
+    for (int j = 0; j < 4; j++) {
+        w[j] = weight(c[j] ? ROW::bin_value(pos_bits(pos + j), weight.largest()) : weight.largest());
+        __builtin_amdgcn_sched_barrier(0);  // one at a time: four at once take the registers that hold the row
+    }
 }
 
 // Lists the blocks that hold candidates and notes the first; where asked,
@@ -503,21 +541,22 @@ __device__ __forceinline__ void survey(HistShared &sh, int wide, bool sum_up) {
     }
 }
 
-// Totals of the listed blocks, a block a wave.
-template <class ROW>
+// Totals of the listed blocks, a block a wave: candidates, and with MASS their weights.
+template <class ROW, bool MASS>
 __device__ __forceinline__ void total(HistShared &sh, int wide, const Weight &weight) {
     const int wave = threadIdx.x >> 6, n = (int)sh.n_blocks;
     for (int e = wave; e < n; e += kRowWaves) {
         const int b = sh.blocks[e];
         uint32_t c[4];
-        double w[4];
         bins(sh, wide, b, c);
-        bin_weights<ROW>(weight, b, c, w);
-        const double m = wave_scan(((double)c[0] * w[0] + (double)c[1] * w[1]) + ((double)c[2] * w[2] + (double)c[3] * w[3]));
         const int s = wave_scan((int)(c[0] + c[1] + c[2] + c[3]));
-        if ((threadIdx.x & 63) == 63) {
-            sh.blk_cnt[b] = (uint32_t)s;
-            sh.blk_mass[b] = m;
+        if ((threadIdx.x & 63) == 63) sh.blk_cnt[b] = (uint32_t)s;
+        if (MASS) {
+            double w[4];
+            bin_weights<ROW>(weight, b, c, w);
+            const double m =
+                wave_scan(((double)c[0] * w[0] + (double)c[1] * w[1]) + ((double)c[2] * w[2] + (double)c[3] * w[3]));
+            if ((threadIdx.x & 63) == 63) sh.blk_mass[b] = m;
         }
     }
 }
@@ -562,7 +601,7 @@ __device__ __forceinline__ uint32_t total_wide(HistShared &sh, const uint16_t *x
         survey(sh, sign, false);
         __syncthreads();
         if (top == 0xFFFFFFFFu && sh.top_block != 0xFFFFFFFFu) top = top_position(sh, sign);
-        total<ROW>(sh, sign, Weight{(double)bits_value(pos_bits(top)), inv_t});
+        total<ROW, true>(sh, sign, Weight(bits_value(pos_bits(top)), inv_t));
     }
     return top;
 }
@@ -592,6 +631,7 @@ struct HistOrder {
     __device__ __forceinline__ HistOrder(HistShared &s, ROW &r) : sh(s), row(r) {}
 
     // Reads, counts and orders the row under weights 1 / T.  False: no candidate.
+    template <bool MASS>
     __device__ __forceinline__ bool build(double inv_t) {
         const int t = threadIdx.x;
         wide = -1;
@@ -631,21 +671,32 @@ struct HistOrder {
                 return false;
             }
             if (top_pos_ == 0xFFFFFFFFu) return false;
-            weight = Weight{(double)bits_value(pos_bits(top_pos_)), inv_t};
+            weight = Weight(bits_value(pos_bits(top_pos_)), inv_t);
         } else {
             if (sh.top_block == 0xFFFFFFFFu || overflowed) return false;
-            weight = Weight{(double)value_of_key(sh.top_key), inv_t};
+            weight = Weight(value_of_key(sh.top_key), inv_t);
         }
-        if (wide < 0) total<ROW>(sh, -1, weight);
+        if (wide < 0) total<ROW, MASS>(sh, -1, weight);
         __syncthreads();
         if (searches()) {
             uint32_t bc[4];
             double bm[4];
             blocks(bc, bm);
             incl = (uint32_t)wave_scan((int)(bc[0] + bc[1] + bc[2] + bc[3]));
-            mass_incl = wave_scan((bm[0] + bm[1]) + (bm[2] + bm[3]));
+            mass_incl = MASS ? wave_scan((bm[0] + bm[1]) + (bm[2] + bm[3])) : 0.0;
         }
         return true;
+    }
+    // The masses of a row built without them; every wave calls it.
+    __device__ __forceinline__ void add_masses() {
+        total<ROW, true>(sh, -1, weight);
+        __syncthreads();
+        if (searches()) {
+            uint32_t bc[4];
+            double bm[4];
+            blocks(bc, bm);
+            mass_incl = wave_scan((bm[0] + bm[1]) + (bm[2] + bm[3]));
+        }
     }
     // (These read other lanes: every lane calls them.)
     __device__ bool searches() const { return wide >= 0 || threadIdx.x < 64; }
@@ -730,6 +781,49 @@ struct HistOrder {
         for (int j = 0; j < 4; j++) n += 4 * lane + j <= at ? c[j] : 0u;
         return before + (uint32_t)lane_int(wave_scan((int)n), 63);
     }
+    // The same by rank without masses.
+    __device__ __forceinline__ HistPlace find_rank(uint32_t rank) {
+        const int lane = threadIdx.x & 63;
+        HistPlace q;
+        q.mass_above = q.w = 0.0;
+        uint32_t c[4];
+        const uint4 v = ((const uint4 *)sh.blk_cnt)[lane];
+        c[0] = v.x; c[1] = v.y; c[2] = v.z; c[3] = v.w;
+        uint32_t before = 0, in = incl;
+#pragma unroll
+        for (int step = 0; step < 2; step++) {
+            const uint32_t own = c[0] + c[1] + c[2] + c[3];
+            const uint64_t f = __ballot(own != 0), h = __ballot(own != 0 && before + in > rank);
+            const int L = h ? __builtin_ctzll(h) : f ? 63 - __builtin_clzll(f) : 0;
+            // every lane looks at its own four as if it were the one: the
+            // first that reaches the rank, else the last with a candidate
+            uint32_t sum = before + in - own, at = 0, sum_at = sum, c_at = 0;
+            bool done = false;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const bool is = !done && c[j] != 0;
+                at = is ? j : at;
+                sum_at = is ? sum : sum_at;
+                c_at = is ? c[j] : c_at;
+                sum += c[j];
+                done = done || (is && sum > rank);
+            }
+            before = (uint32_t)lane_int((int)sum_at, L);
+            q.count = (uint32_t)lane_int((int)c_at, L);
+            const int i = 4 * L + lane_int((int)at, L);
+            if (step == 0) {
+                q.pos = (uint32_t)i;
+                hold(i);
+                bins(sh, wide, i, c);
+                in = (uint32_t)wave_scan((int)(c[0] + c[1] + c[2] + c[3]));
+            } else {
+                q.pos = q.pos * 256 + i;
+            }
+        }
+        q.above = before;
+        return q;
+    }
+
     // Mass of the positions up to pos, its own included.
     __device__ __forceinline__ double mass_to(uint32_t pos) {
         const int b = pos >> 8, lane = threadIdx.x & 63, at = (int)(pos & 255u);

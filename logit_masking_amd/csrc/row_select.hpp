@@ -48,10 +48,11 @@ struct RowView {
     }
 };
 
-// e^y for y <= 0 (and a little above) to within two units of a double's last
-// place; 0 for NaN.  y = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts, so
-// that r is exact), e^r by its power series to r^13 / 13! (the next term is
-// under 2^-57), times 2^n.
+// e^y for y <= 0 (and a little above) to 2^-42 of itself; 0 for NaN.  y = n ln 2
+// + r with |r| <= ln 2 / 2 (ln 2 in two parts, so that r is exact), e^r by its
+// power series to r^10 / 10! (the next term is under 2^-42), times 2^n.  A mass
+// of 2^18 such weights moves by 2^-42 of itself: the chance that this moves a
+// draw over a border between 10^5 candidates is 10^-7.
 //
 // Its constants are put into scalar registers where they are used: kept in
 // vector registers over the kernels' loops they are 30 of a thread's 128.
@@ -64,10 +65,7 @@ __device__ __forceinline__ double exp_falling(double y) {
     const double n = rint(y * scalar(1.4426950408889634074));
     double r = fma(-n, scalar(6.93147180369123816490e-01), y);
     r = fma(-n, scalar(1.90821492927058770002e-10), r);
-    double p = scalar(1.0 / 6227020800.0);
-    p = fma(p, r, scalar(1.0 / 479001600.0));
-    p = fma(p, r, scalar(1.0 / 39916800.0));
-    p = fma(p, r, scalar(1.0 / 3628800.0));
+    double p = scalar(1.0 / 3628800.0);
     p = fma(p, r, scalar(1.0 / 362880.0));
     p = fma(p, r, scalar(1.0 / 40320.0));
     p = fma(p, r, scalar(1.0 / 5040.0));
@@ -108,13 +106,18 @@ __device__ __forceinline__ double log_of(double s) {
     return fma((double)e, scalar(0.693147180559945309), 2.0 * p);
 }
 
-// Weight of a candidate under temperature: 1 at the maximum.  Where m = +inf
-// meets T = +inf the exponent is NaN: all weight is m's.
+// Weight of a candidate under temperature: 1 at the maximum.  +inf counts as
+// 1e300, so that at a maximum of +inf it weighs 1 and all else 0.
 struct Weight {
     double m, inv_t;  // largest logit; 1 / T (1 for greedy rows)
-    __device__ __forceinline__ double operator()(float x) const {
-        return (double)x == m ? 1.0 : exp_falling(((double)x - m) * inv_t);
+    __device__ __forceinline__ Weight() {}
+    __device__ __forceinline__ Weight(float largest, double inv) {
+        m = fmin((double)largest, 1e300);
+        inv_t = m < 1e300 ? inv : fmax(inv, 1e-200);
     }
+    __device__ __forceinline__ double exponent(float x) const { return (fmin((double)x, 1e300) - m) * inv_t; }
+    __device__ __forceinline__ double operator()(float x) const { return exp_falling(exponent(x)); }
+    __device__ __forceinline__ float largest() const { return (float)m; }  // (1e300 is +inf again)
 };
 constexpr double kMassUnit = 0x1p40;
 __device__ __forceinline__ uint64_t fixed_mass(double w) { return __double2ull_rn(w * kMassUnit); }

@@ -61,7 +61,7 @@ __device__ void top_by_digits(const TopArgs &a, int r, DigitsShared &ds) {
     const uint32_t best = row_max_key(row, sh);
     uint64_t mass = 0;
     if (best) {
-        const Weight weight{(double)value_of_key(best), 1.0};
+        const Weight weight(value_of_key(best), 1.0);
         mass = row_mass(row, weight, 0u, sh);
         const Place q = row_find<DT, false>(row, weight, (uint32_t)a.k - 1, 0, sh);
         const uint32_t ties = min(q.count, (uint32_t)a.k - q.above);
@@ -148,9 +148,9 @@ __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
     HistOrder<HistRow<NP, SPANS>> order(sh, row);
     uint64_t *list = (uint64_t *)sh.h;
     uint32_t n = 0;
-    if (order.build(1.0)) {
+    if (order.template build<true>(1.0)) {
         if (order.searches()) {
-            const HistPlace q = order.template find<0>((uint32_t)a.k - 1, 0.0);
+            const HistPlace q = order.find_rank((uint32_t)a.k - 1);
             const double mass = order.total_mass();
             if (threadIdx.x == 0) {
                 sh.place = q;
@@ -197,12 +197,12 @@ __global__ __launch_bounds__(kRowThreads) void k_top_fine(TopArgs a) {
     HistOrder<FineRow<NP, SPANS, true>> order(sh, row);
     uint64_t *list = (uint64_t *)sh.h;
     uint32_t n = 0;
-    if (order.build(1.0)) {
+    if (order.template build<false>(1.0)) {
         const double part = row.run_sum ? (double)row.run_sum * exp_falling((double)row.run_max - order.weight.m) : 0.0;
         const double whole = wave_scan(part);
         if ((threadIdx.x & 63) == 63) more.sum[threadIdx.x >> 6] = whole;
         if (order.searches()) {
-            const HistPlace q = order.template find<0>((uint32_t)a.k - 1, 0.0);
+            const HistPlace q = order.find_rank((uint32_t)a.k - 1);
             if (threadIdx.x == 0) {
                 sh.place = q;
                 sh.n_list = 0;
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(kRowThreads) void k_top_fine(TopArgs a) {
         if (threadIdx.x == 0) {
             double s = 0.0;
             for (int w = 0; w < kRowWaves; w++) s += more.sum[w];
-            a.lse[r] = (float)(order.weight.m < INFINITY ? order.weight.m + log_of(s) : INFINITY);
+            a.lse[r] = order.weight.largest() < INFINITY ? (float)(order.weight.m + log_of(s)) : INFINITY;
         }
         const HistPlace q = sh.place;
         n = q.above + q.count;
@@ -221,9 +221,10 @@ __global__ __launch_bounds__(kRowThreads) void k_top_fine(TopArgs a) {
             top_by_digits<0>(a, r, more.digits);
             return;
         }
-        const uint32_t key_lo = (65535u - q.pos) << 16;
-        row.each([&](uint32_t key, int id) {
-            if (key >= key_lo) list[atomicAdd(&sh.n_list, 1u)] = (uint64_t)~key << 32 | (uint32_t)id;
+        const float x_lo = bin_low(q.pos);
+        row.each([&](float x, int id) {
+            if (x >= x_lo)
+                list[atomicAdd(&sh.n_list, 1u)] = (uint64_t)~key_of_bits(__float_as_uint(x)) << 32 | (uint32_t)id;
         });
     } else if (order.overflowed) {
         __syncthreads();
