@@ -25,19 +25,24 @@ struct FilterArgs {
     float *logprob;
 };
 
+// Under a temperature above this the lowest value of a type weighs something
+// beside others: such rows are searched by digits (row_hist.hpp).
+constexpr float kEvenT = 1e30f;
+
 // Every filter keeps a prefix of the row's order (row_select.hpp), so the
 // kept set is a place: all candidates of larger keys than `key`, and the
 // first `ties` of those equal to it.
 struct Cut {
     uint32_t key, ties;
 };
-// The whole draw digit by digit (row_select.hpp), for rows that the windows do
-// not take: a bin of float32 logits with more candidates than a window.
+// The whole draw digit by digit (row_select.hpp), for rows that the counts and
+// windows do not take: one value over and over, a bin of float32 logits with
+// more candidates than a window, nothing but a type's lowest value.
 template <int DT>
 __device__ void filter_by_digits(const FilterArgs &a, int r, SelectShared &sh) {
     RowView<DT> row{(const char *)a.logits + (size_t)r * (size_t)a.stride * (DT == 0 ? 4 : 2),
                     a.mask ? a.mask + (size_t)r * a.wpr : nullptr, a.V};
-    const float T = a.temp[r];
+    const float T = uniform(a.temp[r]);
     const bool greedy = !(T > 0.f);
     const uint32_t best = row_max_key(row, sh);
     if (best == 0) {
@@ -48,9 +53,9 @@ __device__ void filter_by_digits(const FilterArgs &a, int r, SelectShared &sh) {
         return;
     }
     const Weight weight(value_of_key(best), greedy ? 1.0 : 1.0 / (double)T);
-    const int k = a.top_k ? a.top_k[r] : 0;
-    const float p = a.top_p ? a.top_p[r] : 1.f;
-    const float mp = a.min_p ? a.min_p[r] : 0.f;
+    const int k = a.top_k ? uniform(a.top_k[r]) : 0;
+    const float p = a.top_p ? uniform(a.top_p[r]) : 1.f;
+    const float mp = a.min_p ? uniform(a.min_p[r]) : 0.f;
 
     Cut cut{0, 0};  // below every candidate: all kept
     uint64_t mass;
@@ -185,14 +190,21 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     HistRow<NP, SPANS> row;
     row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
              a.wpr, a.V);
-    const float T = a.temp[r];
-    const int k = a.top_k ? a.top_k[r] : 0;
-    const float p = a.top_p ? a.top_p[r] : 1.f;
-    const float mp = a.min_p ? a.min_p[r] : 0.f;
-    const float u = a.uniform[r];
+    const float T = uniform(a.temp[r]);
+    const int k = a.top_k ? uniform(a.top_k[r]) : 0;
+    const float p = a.top_p ? uniform(a.top_p[r]) : 1.f;
+    const float mp = a.min_p ? uniform(a.min_p[r]) : 0.f;
+    const float u = uniform(a.uniform[r]);
     const bool greedy = !(T > 0.f);
-    HistOrder<HistRow<NP, SPANS>> order(sh, row);
-    if (!order.template build<true>(greedy ? 1.0 : 1.0 / (double)T)) {
+    typedef HistOrder<HistRow<NP, SPANS>> Order;
+    Order order(sh, row);
+    const auto found = T > kEvenT ? Order::kByDigits : order.template build<true>(greedy ? 1.0 : 1.0 / (double)T);
+    if (found == Order::kByDigits) {
+        __syncthreads();
+        filter_by_digits<1>(a, r, *(SelectShared *)sh.h);
+        return;
+    }
+    if (found == Order::kNone) {
         if (threadIdx.x == 0) {
             a.ids[r] = -1;
             a.logprob[r] = 0.f;
@@ -210,8 +222,8 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
         }
     }
     __syncthreads();
-    const uint32_t pos = sh.place.pos, count = sh.place.count, n = sh.n;
-    const double mass = sh.mass;
+    const uint32_t pos = uniform(sh.place.pos), count = uniform(sh.place.count), n = uniform(sh.n);
+    const double mass = uniform(sh.mass);
     const int id = row.nth(pos, count, n, sh);
     if (threadIdx.x == 0) {
         const double y = order.weight.exponent(bits_value(pos_bits(pos)));
@@ -224,36 +236,35 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
 template <int NP, bool SPANS>
 __global__ __launch_bounds__(kRowThreads) void k_filter_fine(FilterArgs a) {
     __shared__ HistShared sh;
-    __shared__ union {
-        FineShared fine;
-        SelectShared select;
-    } more;
-    FineShared &fs = more.fine;
+    __shared__ FineShared fs;
     const int r = blockIdx.x;
     FineRow<NP, SPANS, false> row;
     row.init((const float *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr, a.V);
-    const float T = a.temp[r];
-    const int k = a.top_k ? a.top_k[r] : 0;
-    const float p = a.top_p ? a.top_p[r] : 1.f;
-    const float mp = a.min_p ? a.min_p[r] : 0.f;
-    const float u = a.uniform[r];
+    const float T = uniform(a.temp[r]);
+    const int k = a.top_k ? uniform(a.top_k[r]) : 0;
+    const float p = a.top_p ? uniform(a.top_p[r]) : 1.f;
+    const float mp = a.min_p ? uniform(a.min_p[r]) : 0.f;
+    const float u = uniform(a.uniform[r]);
     const bool greedy = !(T > 0.f);
-    HistOrder<FineRow<NP, SPANS, false>> order(sh, row);
-    int i = -1;
-    double mass = 0.0;
-    if (order.template build<false>(greedy ? 1.0 : 1.0 / (double)T)) {
-        FineDraw<FineRow<NP, SPANS, false>> fine{order, fs};
-        i = fine.draw(greedy, k, p, mp, u, mass);
-    } else if (!order.overflowed) {
+    typedef HistOrder<FineRow<NP, SPANS, false>> Order;
+    Order order(sh, row);
+    const auto found = T > kEvenT ? Order::kByDigits : order.template build<false>(greedy ? 1.0 : 1.0 / (double)T);
+    if (found == Order::kNone) {
         if (threadIdx.x == 0) {
             a.ids[r] = -1;
             a.logprob[r] = 0.f;
         }
         return;
     }
+    int i = -1;
+    double mass = 0.0;
+    if (found == Order::kCounted) {
+        FineDraw<FineRow<NP, SPANS, false>> fine{order, fs};
+        i = fine.draw(greedy, k, p, mp, u, mass);
+    }
     if (i < 0) {
         __syncthreads();
-        filter_by_digits<0>(a, r, more.select);
+        filter_by_digits<0>(a, r, *(SelectShared *)sh.h);
         return;
     }
     if (threadIdx.x == 0) {

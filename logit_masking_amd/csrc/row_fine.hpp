@@ -18,6 +18,7 @@ namespace cg {
 constexpr int kFinePieceIds = 4 * kRowThreads;  // ids of one 16-byte load of every thread
 constexpr uint32_t kWindow = 1024;              // candidates of a window: one a thread
 constexpr uint32_t kNegInf = 0xFF800000u;
+constexpr uint32_t kLowest32 = 0xFF7FFFFFu;   // the lowest value's bits; only -inf's are larger here
 constexpr uint32_t kLeastKey = 0x00800000u;  // of the type's lowest value
 
 // The row: NP pieces a thread in registers; with SPANS, longer rows in spans
@@ -111,6 +112,7 @@ struct FineRow {
         char *h = (char *)sh.h;
         const uint32_t none = (uint32_t)((char *)&sh.dummy[threadIdx.x & 63] - h);
         float top = -INFINITY;
+        bool any = false;
         const int n_spans = spans();
         for (int span = 0; span < n_spans; span++) {
             uint32_t raw[NP], bits[kWords];
@@ -126,16 +128,32 @@ struct FineRow {
                 for (int j = 0; j < 4; j++) {
                     const uint32_t w = d[p][j];
                     v[j] = __uint_as_float(w);
-                    atomicAdd((uint32_t *)(h + (w != kNegInf ? (w >> 14) & 0x1FFFCu : none)), (int)w < 0 ? 0x10000u : 1u);
+                    atomicAdd((uint32_t *)(h + (w < kLowest32 ? (w >> 14) & 0x1FFFCu : none)), (int)w < 0 ? 0x10000u : 1u);
                 }
                 top = fmaxf(fmaxf(top, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
                 if (SUM) add(v);
                 __builtin_amdgcn_sched_barrier(0);
             }
+            uint32_t some = 0;
+#pragma unroll
+            for (int i = 0; i < kWords; i++) some |= bits[i];
+            any = any || some != 0;
         }
 #pragma unroll
         for (int s = 32; s; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
+        if (__any(any) && (threadIdx.x & 63) == 0) sh.any = 1;
         if ((threadIdx.x & 63) == 0 && top > -INFINITY) atomicMax(&sh.top_key, key_of_bits(__float_as_uint(top)));
+    }
+    // Whether the row holds the type's lowest value.  Every thread calls it.
+    __device__ __forceinline__ bool has_lowest(HistShared &sh) {
+        bool has = false;
+        each([&](float x, int) { has = has || __float_as_uint(x) == kLowest32; });
+        __syncthreads();
+        if (threadIdx.x == 0) sh.any = 0;
+        __syncthreads();
+        if (__any(has) && (threadIdx.x & 63) == 0) sh.any = 1;
+        __syncthreads();
+        return sh.any != 0;
     }
     // f(x, id) for every element; what is no candidate is -inf.
     template <class F>
@@ -161,9 +179,10 @@ struct FineRow {
 
 // The smallest and the largest value of a bin.  Position 32767 is both zeros'
 // and holds what is nearer to them than a bin's width, on both sides; the
-// infinite one's bounds are infinite.
+// infinite one's bounds are infinite; the last one's lowest value is not
+// counted.
 __device__ __forceinline__ float bin_low(uint32_t pos) {
-    return pos == 32767u ? value_of_key(0x7FFF0000u) : pos < 128u ? INFINITY : value_of_key((65535u - pos) << 16);
+    return pos == kLowest ? value_of_key(kLeastKey + 1) : pos == 32767u ? value_of_key(0x7FFF0000u) : pos < 128u ? INFINITY : value_of_key((65535u - pos) << 16);
 }
 __device__ __forceinline__ float bin_high(uint32_t pos) {
     return pos < 128u ? INFINITY : value_of_key((65535u - pos) << 16 | 0xFFFFu);
@@ -229,7 +248,7 @@ struct FineDraw {
         v += __shfl_xor(v, 4);
         v += __shfl_xor(v, 8);
         __syncthreads();
-        return v;
+        return uniform(v);
     }
 
     // Sorts the list by the bins' own counts: each entry goes to its bin's
@@ -284,7 +303,7 @@ struct FineDraw {
     __device__ __forceinline__ uint32_t bin_count(uint32_t pos) const {
         const uint32_t i = pos_bits(pos) & 0x7FFFu;
         uint32_t cp, cn;
-        cleaned(-1, (int)i, order.sh.h[i], cp, cn);
+        cleaned((int)i, order.sh.h[i], cp, cn);
         return pos < 32768u ? cp : cn;
     }
 
@@ -336,7 +355,7 @@ struct FineDraw {
             if (t == 0) fs.n = c;
         }
         __syncthreads();
-        const uint32_t count = fs.n;
+        const uint32_t count = uniform(fs.n);
         __syncthreads();
         // the window: positions lo .. hi hold the n listed candidates, `above` and mass_above lie before
         uint32_t lo = 0, hi = 0, above = 0, n = 0;
@@ -368,9 +387,9 @@ struct FineDraw {
                         }
                     }
                     __syncthreads();
-                    key = fs.key;
-                    c_before = fs.before;
-                    c_end = fs.end;
+                    key = uniform(fs.key);
+                    c_before = uniform(fs.before);
+                    c_end = uniform(fs.end);
                     if (c_before >= kept) stage = kTotal;  // it keeps them all
                 }
             }
@@ -396,16 +415,16 @@ struct FineDraw {
                         fs.hit = (int)t;
                     __syncthreads();
                     have = true;
-                    i = fs.hit;
+                    i = uniform(fs.hit);
                 }
             } else if (by_mass && n) {
-                const double end = mass_above + fs.mass[n - 1];
+                const double end = mass_above + uniform(fs.mass[n - 1]);
                 if (lo > 0 && reached(mass_above)) {
                     to = min(to, lo - 1);
-                    guess = valued ? fs.value[0] * (target / mass_above) : target / scale;
+                    guess = valued ? uniform(fs.value[0]) * (target / mass_above) : target / scale;
                 } else if (!reached(end) && above + n < count) {
                     from = max(from, hi + 1);
-                    guess = valued ? fs.value[1] + (target - end) / scale : target / scale;
+                    guess = valued ? uniform(fs.value[1]) + (target - end) / scale : target / scale;
                 } else {
                     // the first that reaches it, else the last with weight
                     __syncthreads();
@@ -419,7 +438,7 @@ struct FineDraw {
                     }
                     __syncthreads();
                     have = true;
-                    i = fs.hit;
+                    i = uniform(fs.hit);
                 }
             }
             // from the row
@@ -435,7 +454,7 @@ struct FineDraw {
                             if (t == 0) fs.value[0] = m;
                         }
                         __syncthreads();
-                        scale = base / fs.value[0];
+                        scale = base / uniform(fs.value[0]);
                         __syncthreads();
                     }
                 }
@@ -459,10 +478,10 @@ struct FineDraw {
                         }
                     }
                     __syncthreads();
-                    if (!fs.fits) return -1;
-                    lo = fs.lo;
-                    hi = fs.hi;
-                    above = fs.above;
+                    if (!uniform(fs.fits)) return -1;
+                    lo = uniform(fs.lo);
+                    hi = uniform(fs.hi);
+                    above = uniform(fs.above);
                     x_hi = bin_high(lo);
                     x_lo = bin_low(hi);
                 }
@@ -486,7 +505,7 @@ struct FineDraw {
                     continue;
                 }
                 mass_above = s;
-                n = min(fs.n, kWindow);
+                n = min(uniform(fs.n), kWindow);
                 sort_window(lo, hi, n);
                 const double w = t < n ? order.weight(value_of_key(~(uint32_t)(fs.list[t] >> 32))) : 0.0;
                 const double m = wave_scan(w);
@@ -509,7 +528,7 @@ struct FineDraw {
             }
             // the stage's answer, and the next stage
             const uint32_t end = above + (uint32_t)i + 1;
-            const double m_end = mass_above + fs.mass[i];
+            const double m_end = mass_above + uniform(fs.mass[i]);
             if (stage == kTopK) {
                 kept = (uint32_t)k;
                 base = mass = m_end;

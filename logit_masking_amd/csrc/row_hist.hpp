@@ -12,8 +12,11 @@
 // Counts are 16 bits, 128 KB of LDS: dword i holds the counts of the value
 // with bits i in its low half and of its negative in the high one.  A count
 // can only overflow in a row of 65536 candidates or more; the carry breaks
-// the sum of all counts, which is checked, and such a row is counted again
-// in 32 bits, one sign at a time (`wide`; -0 with the positives).
+// the sum of all counts, which is checked, and such a row is left to the
+// search by digits (row_select.hpp).  The type's lowest value, which many
+// programs write where a logit is masked, is not counted: it weighs nothing
+// beside any other candidate; a row that has nothing else, or of which it is
+// asked for, goes the same way.
 //
 // Order positions run from the largest value down: position p < 32768 is the
 // value of bits 32767 - p, the others the negatives, magnitude rising.  The
@@ -28,6 +31,7 @@ constexpr int kHistDwords = 32768, kHistBlocks = 256;
 constexpr int kPieceIds = 8 * kRowThreads;  // ids of one 16-byte load of every thread
 constexpr int kNegInfPair = (int)0xFF80FF80;
 constexpr int kInfIdx = 0x7F80;             // bits of +inf; larger ones are NaN
+constexpr uint32_t kLowest = 0xFF7Fu;       // bits of the lowest value; larger ones are -inf and NaN
 constexpr int kBufWord3 = 0x00020000;       // raw buffer, 32-bit data format
 
 // A place in the order: the position, its candidates, those before it, their mass.
@@ -43,6 +47,7 @@ struct HistShared {
     uint32_t blk_cnt[kHistBlocks];
     double blk_mass[kHistBlocks];
     uint32_t counted;    // sum of every count, the dummies' included
+    uint32_t any;        // the row has an allowed id
     uint32_t top_block;  // first block with a candidate
     uint32_t top_key;    // key of the largest candidate (rows of float32)
     uint32_t n_blocks;   // blocks with a candidate, listed in any order
@@ -238,11 +243,14 @@ struct HistRow {
 #pragma unroll
             for (int i = 0; i < kWords; i++) bytes[i] = bytes_next[i];
         }
-        if ((threadIdx.x & 63) == 0 && dead) atomicAdd(&sh.counted, dead * 512u);  // of one wave
+        if ((threadIdx.x & 63) == 0) {
+            if (dead) atomicAdd(&sh.counted, dead * 512u);  // of one wave
+            if (dead < (uint32_t)(NP * n_spans)) sh.any = 1;
+        }
     }
 
-    // Counts a piece.  -inf and negative NaNs go to the lane's own dummy (a
-    // run of one value would queue at one address).
+    // Counts a piece.  The lowest value, -inf and negative NaNs go to the
+    // lane's own dummy (a run of one value would queue at one address).
     __device__ __forceinline__ void count(int p, HistShared &sh) {
         char *h = (char *)sh.h;
         const uint32_t none = (uint32_t)((char *)&sh.dummy[threadIdx.x & 63] - h);
@@ -250,8 +258,8 @@ struct HistRow {
         for (int j = 0; j < 4; j++) {
             const uint32_t w = d[p][j];
             const uint32_t a0 = (w << 2) & 0x1FFFCu, a1 = (w >> 14) & 0x1FFFCu;
-            atomicAdd((uint32_t *)(h + ((uint16_t)w < 0xFF80u ? a0 : none)), (w & 0x8000u) ? 0x10000u : 1u);
-            atomicAdd((uint32_t *)(h + (w < 0xFF800000u ? a1 : none)), (int)w < 0 ? 0x10000u : 1u);
+            atomicAdd((uint32_t *)(h + ((uint16_t)w < kLowest ? a0 : none)), (w & 0x8000u) ? 0x10000u : 1u);
+            atomicAdd((uint32_t *)(h + (w < kLowest << 16 ? a1 : none)), (int)w < 0 ? 0x10000u : 1u);
         }
     }
 
@@ -300,6 +308,31 @@ struct HistRow {
         }
     }
 
+    // Whether the row holds the type's lowest value.  Every thread calls it.
+    __device__ __forceinline__ bool has_lowest(HistShared &sh) {
+        const uint32_t want = kLowest | kLowest << 16;
+        bool has = false;
+        const int n_spans = spans();
+        for (int s = 0; s < n_spans; s++) {
+            if (SPANS && s) load(s - 1, sh.lut);
+#pragma unroll
+            for (int p = 0; p < NP; p++) {
+                if (!((live >> p) & 1)) continue;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const uint32_t y = d[p][j] ^ want;
+                    has = has || (uint16_t)y == 0 || y < 0x10000u;
+                }
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) sh.any = 0;
+        __syncthreads();
+        if (__any(has) && (threadIdx.x & 63) == 0) sh.any = 1;
+        __syncthreads();
+        return uniform(sh.any) != 0;
+    }
+
     // Lists the first `upto` candidates of position pos by rising id, reading
     // the row again 1024 ids at a time (more of one value than the list takes).
     __device__ void first_of(uint32_t pos, uint32_t upto, uint64_t *list, HistShared &sh) const {
@@ -314,8 +347,9 @@ struct HistRow {
             if (lane == 0) sh.w_cnt[wave] = __popcll(hits);
             __syncthreads();
             uint32_t mine = before;
+#pragma unroll 1
             for (int w = 0; w < kRowWaves; w++) {
-                const uint32_t c = sh.w_cnt[w];
+                const uint32_t c = uniform(sh.w_cnt[w]);
                 mine += w < wave ? c : 0;
                 before += c;
             }
@@ -350,7 +384,7 @@ struct HistRow {
     __device__ __forceinline__ int nth(uint32_t pos, uint32_t count, uint32_t n, HistShared &sh) {
         typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
         const Match match(pos);
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_spans = spans();
+        const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), n_spans = spans();
         uint32_t *const cnt = sh.list;  // by piece, then wave
         static_assert(NP * kRowWaves <= kRowThreads, "the counts fit");
         uint32_t before = 0;  // in the spans looked at
@@ -430,7 +464,7 @@ struct HistRow {
             before += all;
         }
         __syncthreads();
-        return sh.found;
+        return uniform(sh.found);
     }
 };
 
@@ -440,19 +474,17 @@ __device__ __forceinline__ void clear_counts(HistShared &sh) {
     for (int i = 0; i < kHistDwords / 4 / kRowThreads; i++) h[threadIdx.x + i * kRowThreads] = make_uint4(0, 0, 0, 0);
 }
 
-// What dword i counts, without NaN, both zeros as the positive one.  wide: -1:
-// both signs in 16 bits, 0 / 1: that sign in 32.
-__device__ __forceinline__ void cleaned(int wide, int i, uint32_t c, uint32_t &pos, uint32_t &neg) {
-    pos = wide < 0 ? c & 0xFFFFu : wide == 0 ? c : 0u;
-    neg = wide < 0 ? c >> 16 : wide == 1 ? c : 0u;
-    if (i > kInfIdx) pos = 0;
+// What dword i counts, without NaN, both zeros as the positive one.
+__device__ __forceinline__ void cleaned(int i, uint32_t c, uint32_t &pos, uint32_t &neg) {
+    pos = i > kInfIdx ? 0u : c & 0xFFFFu;
+    neg = c >> 16;
     if (i == 0) {
         pos += neg;
         neg = 0;
     }
 }
 // Candidates of the lane's four order positions of a block, b * 256 + 4 lane + j.
-__device__ __forceinline__ void bins(const HistShared &sh, int wide, int b, uint32_t (&c)[4]) {
+__device__ __forceinline__ void bins(const HistShared &sh, int b, uint32_t (&c)[4]) {
     const int lane = threadIdx.x & 63;
     const bool neg = b >= kHistBlocks / 2;  // uniform
     const int q = neg ? (b - kHistBlocks / 2) * 64 + lane : (kHistBlocks / 2 - 1 - b) * 64 + 63 - lane;
@@ -462,7 +494,7 @@ __device__ __forceinline__ void bins(const HistShared &sh, int wide, int b, uint
     for (int j = 0; j < 4; j++) {
         uint32_t cp, cn;
         const int at = neg ? j : 3 - j;
-        cleaned(wide, q * 4 + at, neg ? d[j] : d[3 - j], cp, cn);
+        cleaned(q * 4 + at, neg ? d[j] : d[3 - j], cp, cn);
         c[j] = neg ? cn : cp;
     }
 }
@@ -496,8 +528,8 @@ __device__ __forceinline__ void bin_weights(const Weight &weight, int b, const u
 // Lists the blocks that hold candidates and notes the first; where asked,
 // sums all counts.  A wave takes 256 dwords at a time, 4 a lane: a block of
 // positives and one of negatives.
-__device__ __forceinline__ void survey(HistShared &sh, int wide, bool sum_up) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__device__ __forceinline__ void survey(HistShared &sh, bool sum_up) {
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
     const uint4 *h4 = (const uint4 *)sh.h;
     uint32_t sum = 0;
 #pragma unroll
@@ -513,15 +545,14 @@ __device__ __forceinline__ void survey(HistShared &sh, int wide, bool sum_up) {
                 sum = add_halves(c[i].z, add_halves(c[i].w, sum));
             }
             const uint32_t all = c[i].x | c[i].y | c[i].z | c[i].w;
-            uint32_t pos = wide < 0 ? all & 0xFFFFu : wide == 0 ? all : 0u;
-            uint32_t neg = wide < 0 ? all >> 16 : wide == 1 ? all : 0u;
+            uint32_t pos = all & 0xFFFFu, neg = all >> 16;
             if (g == 0 || g == kHistDwords / 256 - 1) {  // zeros and NaNs
                 pos = neg = 0;
                 const uint32_t v[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     uint32_t cp, cn;
-                    cleaned(wide, g * 256 + lane * 4 + j, v[j], cp, cn);
+                    cleaned(g * 256 + lane * 4 + j, v[j], cp, cn);
                     pos |= cp;
                     neg |= cn;
                 }
@@ -543,12 +574,12 @@ __device__ __forceinline__ void survey(HistShared &sh, int wide, bool sum_up) {
 
 // Totals of the listed blocks, a block a wave: candidates, and with MASS their weights.
 template <class ROW, bool MASS>
-__device__ __forceinline__ void total(HistShared &sh, int wide, const Weight &weight) {
-    const int wave = threadIdx.x >> 6, n = (int)sh.n_blocks;
+__device__ __forceinline__ void total(HistShared &sh, const Weight &weight) {
+    const int wave = uniform((int)(threadIdx.x >> 6)), n = uniform((int)sh.n_blocks);
     for (int e = wave; e < n; e += kRowWaves) {
-        const int b = sh.blocks[e];
+        const int b = uniform((int)sh.blocks[e]);
         uint32_t c[4];
-        bins(sh, wide, b, c);
+        bins(sh, b, c);
         const int s = wave_scan((int)(c[0] + c[1] + c[2] + c[3]));
         if ((threadIdx.x & 63) == 63) sh.blk_cnt[b] = (uint32_t)s;
         if (MASS) {
@@ -562,61 +593,23 @@ __device__ __forceinline__ void total(HistShared &sh, int wide, const Weight &we
 }
 
 // The largest candidate's position, from the first block.
-__device__ __forceinline__ uint32_t top_position(const HistShared &sh, int wide) {
-    const int b = (int)sh.top_block;
+__device__ __forceinline__ uint32_t top_position(const HistShared &sh) {
+    const int b = uniform((int)sh.top_block);
     uint32_t c[4];
-    bins(sh, wide, b, c);
+    bins(sh, b, c);
     const int first = c[0] ? 0 : c[1] ? 1 : c[2] ? 2 : 3;
     const int lane = __builtin_ctzll(__ballot((c[0] | c[1] | c[2] | c[3]) != 0));
     return b * 256 + lane * 4 + lane_int(first, lane);
 }
 
-// Counts the candidates of one sign in 32 bits.
-__device__ __forceinline__ void recount(HistShared &sh, const uint16_t *x, const uint64_t *mask, int V, int sign) {
-    __syncthreads();
-    clear_counts(sh);
-    __syncthreads();
-#pragma unroll 1
-    for (int i = threadIdx.x; i < V; i += kRowThreads) {
-        if (mask && !((mask[i >> 6] >> (i & 63)) & 1)) continue;
-        const uint32_t v = x[i];
-        if (v >= 0xFF80u || (v > 0x8000u) != (sign != 0)) continue;
-        atomicAdd(&sh.h[v & 0x7FFFu], 1u);
-    }
-    __syncthreads();
-}
-// The totals of a row one of whose counts overflowed; the positives first, so
-// that the largest candidate is known before its weights are needed.  Returns
-// its position; the negatives' counts stay in h.
-template <class ROW>
-__device__ __forceinline__ uint32_t total_wide(HistShared &sh, const uint16_t *x, const uint64_t *mask, int V, double inv_t) {
-    __syncthreads();
-    if (threadIdx.x == 0) sh.top_block = 0xFFFFFFFFu;
-    uint32_t top = 0xFFFFFFFFu;
-#pragma unroll 1
-    for (int sign = 0; sign < 2; sign++) {
-        recount(sh, x, mask, V, sign);
-        if (threadIdx.x == 0) sh.n_blocks = 0;
-        __syncthreads();
-        survey(sh, sign, false);
-        __syncthreads();
-        if (top == 0xFFFFFFFFu && sh.top_block != 0xFFFFFFFFu) top = top_position(sh, sign);
-        total<ROW, true>(sh, sign, Weight(bits_value(pos_bits(top)), inv_t));
-    }
-    return top;
-}
-
 // The counted row: totals by block, and the searches, which one wave runs
 // (a workgroup's worth of waves running them alike costs their instructions
-// sixteen times: 5 us of 35 at 256 rows of 128256).  Only in a row counted
-// one sign at a time do all waves run them, since a search may count again.
+// sixteen times: 5 us of 35 at 256 rows of 128256).
 template <class ROW>
 struct HistOrder {
     HistShared &sh;
     ROW &row;
     Weight weight;
-    bool overflowed;  // (rows of another type than bfloat16: nothing else is known then)
-    int wide;  // -1: h holds both signs in 16 bits; 0 / 1: that sign in 32 bits
     // Candidates and mass up to the end of the lane's blocks 4 lane + j.
     uint32_t incl;
     double mass_incl;
@@ -630,11 +623,11 @@ struct HistOrder {
 
     __device__ __forceinline__ HistOrder(HistShared &s, ROW &r) : sh(s), row(r) {}
 
-    // Reads, counts and orders the row under weights 1 / T.  False: no candidate.
+    // Reads, counts and orders the row under weights 1 / T.
+    enum Found { kNone, kCounted, kByDigits };  // no candidate; all well; not a row for counts
     template <bool MASS>
-    __device__ __forceinline__ bool build(double inv_t) {
+    __device__ __forceinline__ Found build(double inv_t) {
         const int t = threadIdx.x;
-        wide = -1;
         row.read_and_count(sh, [&] {
             clear_counts(sh);
             if (t < 64) sh.dummy[t] = 0;
@@ -651,6 +644,7 @@ struct HistOrder {
             }
             if (t == 0) {
                 sh.counted = 0;
+                sh.any = 0;
                 sh.n_blocks = 0;
                 sh.top_block = 0xFFFFFFFFu;
                 sh.top_key = 0;
@@ -658,25 +652,17 @@ struct HistOrder {
         });
         __syncthreads();
         const bool check = row.V > 65535;  // a count may have overflowed
-        survey(sh, -1, check);
+        survey(sh, check);
         __syncthreads();
-        overflowed = check && sh.counted != (uint32_t)row.spans() * (uint32_t)ROW::kSpan;
+        if (check && uniform(sh.counted) != (uint32_t)row.spans() * (uint32_t)ROW::kSpan) return kByDigits;
+        if (uniform(sh.top_block) == 0xFFFFFFFFu) return uniform(sh.any) ? kByDigits : kNone;
         if constexpr (ROW::kExact) {
-            if (overflowed) {
-                top_pos_ = total_wide<ROW>(sh, row.x, row.mask, row.V, inv_t);
-                wide = 1;
-            } else if (sh.top_block != 0xFFFFFFFFu) {
-                top_pos_ = top_position(sh, -1);
-            } else {
-                return false;
-            }
-            if (top_pos_ == 0xFFFFFFFFu) return false;
-            weight = Weight(bits_value(pos_bits(top_pos_)), inv_t);
+            top_pos_ = top_position(sh);
+            weight = Weight(bits_value(pos_bits(top_pos_)), uniform(inv_t));
         } else {
-            if (sh.top_block == 0xFFFFFFFFu || overflowed) return false;
-            weight = Weight(value_of_key(sh.top_key), inv_t);
+            weight = Weight(uniform(value_of_key(sh.top_key)), uniform(inv_t));
         }
-        if (wide < 0) total<ROW, MASS>(sh, -1, weight);
+        total<ROW, MASS>(sh, weight);
         __syncthreads();
         if (searches()) {
             uint32_t bc[4];
@@ -685,11 +671,11 @@ struct HistOrder {
             incl = (uint32_t)wave_scan((int)(bc[0] + bc[1] + bc[2] + bc[3]));
             mass_incl = MASS ? wave_scan((bm[0] + bm[1]) + (bm[2] + bm[3])) : 0.0;
         }
-        return true;
+        return kCounted;
     }
     // The masses of a row built without them; every wave calls it.
     __device__ __forceinline__ void add_masses() {
-        total<ROW, true>(sh, -1, weight);
+        total<ROW, true>(sh, weight);
         __syncthreads();
         if (searches()) {
             uint32_t bc[4];
@@ -699,7 +685,7 @@ struct HistOrder {
         }
     }
     // (These read other lanes: every lane calls them.)
-    __device__ bool searches() const { return wide >= 0 || threadIdx.x < 64; }
+    __device__ bool searches() const { return threadIdx.x < 64; }
     __device__ uint32_t top_pos() const { return top_pos_; }
     __device__ double total_mass() const { return lane_double(mass_incl, 63); }
     __device__ uint32_t total_count() const { return (uint32_t)lane_int((int)incl, 63); }
@@ -751,8 +737,7 @@ struct HistOrder {
         double w[4], m[4];
         blocks(c, m);
         const int b = pick<HOW>(c, m, incl, mass_incl, rank, mass, q.above, q.mass_above);
-        hold(b);
-        bins(sh, wide, b, c);
+        bins(sh, b, c);
         bin_weights<ROW>(weight, b, c, w);
 #pragma unroll
         for (int j = 0; j < 4; j++) m[j] = (double)c[j] * w[j];
@@ -775,8 +760,7 @@ struct HistOrder {
 #pragma unroll
         for (int j = 0; j < 3; j++) before += j < (b & 3) ? c[j] : 0u;
         before = (uint32_t)lane_int((int)before, b >> 2);
-        hold(b);
-        bins(sh, wide, b, c);
+        bins(sh, b, c);
 #pragma unroll
         for (int j = 0; j < 4; j++) n += 4 * lane + j <= at ? c[j] : 0u;
         return before + (uint32_t)lane_int(wave_scan((int)n), 63);
@@ -813,8 +797,7 @@ struct HistOrder {
             const int i = 4 * L + lane_int((int)at, L);
             if (step == 0) {
                 q.pos = (uint32_t)i;
-                hold(i);
-                bins(sh, wide, i, c);
+                        bins(sh, i, c);
                 in = (uint32_t)wave_scan((int)(c[0] + c[1] + c[2] + c[3]));
             } else {
                 q.pos = q.pos * 256 + i;
@@ -833,8 +816,7 @@ struct HistOrder {
 #pragma unroll
         for (int j = 0; j < 3; j++) before += j < (b & 3) ? w[j] : 0.0;
         before = lane_double(before, b >> 2);
-        hold(b);
-        bins(sh, wide, b, c);
+        bins(sh, b, c);
         bin_weights<ROW>(weight, b, c, w);
 #pragma unroll
         for (int j = 0; j < 4; j++) m += 4 * lane + j <= at ? (double)c[j] * w[j] : 0.0;
@@ -843,16 +825,6 @@ struct HistOrder {
 
   private:
     uint32_t top_pos_;
-
-    // Block b's counts in h (a row counted one sign at a time holds one).
-    __device__ __forceinline__ void hold(int b) {
-        if constexpr (ROW::kExact) {
-            if (wide >= 0 && wide != (b >= kHistBlocks / 2)) {  // uniform
-                wide = b >= kHistBlocks / 2;
-                recount(sh, row.x, row.mask, row.V, wide);
-            }
-        }
-    }
 };
 
 // Launches KERNEL<NP, SPANS> with as many pieces as rows of V ids need (7: the

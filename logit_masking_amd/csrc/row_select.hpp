@@ -22,6 +22,17 @@ namespace cg {
 constexpr int kRowThreads = 1024;
 constexpr int kRowWaves = kRowThreads / 64;
 
+// A value that is alike in every lane, as a scalar: what branches on it then
+// branches for the whole wave, and holds no vector register.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ bool uniform(bool v) { return __builtin_amdgcn_readfirstlane((int)v) != 0; }
+__device__ __forceinline__ float uniform(float v) { return __int_as_float(uniform(__float_as_int(v))); }
+__device__ __forceinline__ double uniform(double v) {
+    const long long u = __double_as_longlong(v);
+    return __longlong_as_double(((long long)uniform((int)(u >> 32)) << 32) | (unsigned)uniform((int)u));
+}
+
 // Keys rise with the float's value; 0 stands for "not a candidate" (below the
 // key of the lowest finite float).
 __device__ __forceinline__ uint32_t key_of_bits(uint32_t b) {
@@ -155,9 +166,10 @@ __device__ uint32_t row_max_key(const RowView<DT> &row, SelectShared &sh) {
     if ((threadIdx.x & 63) == 0) sh.wave[threadIdx.x >> 6] = best;
     __syncthreads();
     best = 0;
+#pragma unroll 1
     for (int w = 0; w < kRowWaves; w++) best = max(best, sh.wave[w]);
     __syncthreads();
-    return best;
+    return uniform(best);
 }
 
 // Mass and number of the candidates of keys >= least.
@@ -176,9 +188,10 @@ __device__ uint64_t row_mass(const RowView<DT> &row, const Weight &weight, uint3
     if ((threadIdx.x & 63) == 0) sh.wave_mass[threadIdx.x >> 6] = s;
     __syncthreads();
     s = 0;
+#pragma unroll 1
     for (int w = 0; w < kRowWaves; w++) s += sh.wave_mass[w];
     __syncthreads();
-    return s;
+    return (uint64_t)uniform((uint32_t)(s >> 32)) << 32 | uniform((uint32_t)s);
 }
 
 // The place of the candidate of rank `rank` (BY_MASS false) or of the first
@@ -198,9 +211,17 @@ __device__ Place row_find(const RowView<DT> &row, const Weight &weight, uint32_t
         for (int i = threadIdx.x; i < row.V; i += kRowThreads) {
             const uint32_t k = row.key(i);
             if (!k || (shift < 24 && (k >> (shift + 8)) != prefix)) continue;
-            const uint32_t d = (k >> shift) & 255u;
-            atomicAdd(&sh.cnt[d], 1u);
-            atomicAdd((unsigned long long *)&sh.mass[d], (unsigned long long)fixed_mass(weight(value_of_key(k))));
+            // lanes that hold the first lane's value count together: a run of one
+            // value would queue at one address
+            const uint32_t d = (k >> shift) & 255u, k0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)k);
+            const uint64_t same = __ballot(k == k0);
+            const uint64_t m = fixed_mass(weight(value_of_key(k)));
+            const uint32_t n = __popcll(same);
+            if (k != k0 || (threadIdx.x & 63) == (uint32_t)__builtin_ctzll(same)) {
+                const uint32_t c = k == k0 ? n : 1u;
+                atomicAdd(&sh.cnt[d], c);
+                atomicAdd((unsigned long long *)&sh.mass[d], (unsigned long long)(m * c));
+            }
         }
         __syncthreads();
         if (threadIdx.x < 64) {  // lane l: the digits 255 - 4l downwards
@@ -245,10 +266,10 @@ __device__ Place row_find(const RowView<DT> &row, const Weight &weight, uint32_t
             }
         }
         __syncthreads();
-        prefix = sh.place.key;
-        above = sh.place.above;
-        mass_above = sh.place.mass_above;
-        count = sh.place.count;
+        prefix = uniform(sh.place.key);
+        above = uniform(sh.place.above);
+        mass_above = (uint64_t)uniform((uint32_t)(sh.place.mass_above >> 32)) << 32 | uniform((uint32_t)sh.place.mass_above);
+        count = uniform(sh.place.count);
         __syncthreads();
     }
     return Place{prefix, count, above, mass_above};
@@ -268,16 +289,17 @@ __device__ int row_nth(const RowView<DT> &row, uint32_t key, uint32_t n, SelectS
         if (lane == 0) sh.wave[wave] = __popcll(hits);
         __syncthreads();
         uint32_t mine = before;
+#pragma unroll 1
         for (int w = 0; w < kRowWaves; w++) {
             if (w < wave) mine += sh.wave[w];
-            before += sh.wave[w];
+            before += uniform(sh.wave[w]);
         }
         mine += __popcll(hits & ((1ull << lane) - 1));
         if (((hits >> lane) & 1) && mine == n) sh.found = i;
         __syncthreads();
         if (before > n) break;  // uniform: every thread has the same sums
     }
-    return sh.found;
+    return uniform(sh.found);
 }
 
 }  // namespace cg

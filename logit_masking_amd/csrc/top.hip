@@ -40,8 +40,9 @@ __device__ void sort_falling(uint64_t *list, int n) {
     __syncthreads();
 }
 
-// The whole row digit by digit (row_select.hpp), for float32 rows with more
-// candidates in the k-th one's bin than the list takes.
+// The whole row digit by digit (row_select.hpp), for rows that the counts do
+// not take (row_hist.hpp), and float32 rows with more candidates in the k-th
+// one's bin than the list takes.
 struct DigitsShared {
     SelectShared select;
     uint64_t list[CG_MAX_TOP];  // key in the high half, the id's complement in the low: one order
@@ -75,9 +76,10 @@ __device__ void top_by_digits(const TopArgs &a, int r, DigitsShared &ds) {
             if (lane == 0) sh.wave[wave] = __popcll(hits);
             __syncthreads();
             uint32_t mine = before;
+#pragma unroll 1
             for (int w = 0; w < kRowWaves; w++) {
                 if (w < wave) mine += sh.wave[w];
-                before += sh.wave[w];
+                before += uniform(sh.wave[w]);
             }
             mine += __popcll(hits & ((1ull << lane) - 1));
             if (key == q.key && mine < ties) list[q.above + mine] = ((uint64_t)key << 32) | (uint32_t)~i;
@@ -145,10 +147,12 @@ __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
     HistRow<NP, SPANS> row;
     row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
              a.wpr, a.V);
-    HistOrder<HistRow<NP, SPANS>> order(sh, row);
+    typedef HistOrder<HistRow<NP, SPANS>> Order;
+    Order order(sh, row);
     uint64_t *list = (uint64_t *)sh.h;
     uint32_t n = 0;
-    if (order.template build<true>(1.0)) {
+    const auto found = order.template build<true>(1.0);
+    if (found == Order::kCounted) {
         if (order.searches()) {
             const HistPlace q = order.find_rank((uint32_t)a.k - 1);
             const double mass = order.total_mass();
@@ -159,7 +163,14 @@ __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
             }
         }
         __syncthreads();
-        const HistPlace q = sh.place;
+        HistPlace q;
+        q.pos = uniform(sh.place.pos);
+        q.above = uniform(sh.place.above);
+        q.count = uniform(sh.place.count);
+        if (q.above + q.count < (uint32_t)a.k && row.has_lowest(sh)) {
+            top_by_digits<1>(a, r, *(DigitsShared *)sh.h);
+            return;
+        }
         // every tie of the last value when they fit, else only the larger
         // candidates here and as many ties as are wanted by their ids
         const bool all = q.above + q.count <= kListRoom;
@@ -175,6 +186,10 @@ __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
             n = min(q.above + q.count, (uint32_t)a.k);
             row.first_of(q.pos, n - q.above, list + q.above, sh);
         }
+    } else if (found == Order::kByDigits) {
+        __syncthreads();
+        top_by_digits<1>(a, r, *(DigitsShared *)sh.h);
+        return;
     } else if (threadIdx.x == 0) {
         a.lse[r] = -INFINITY;
     }
@@ -187,20 +202,19 @@ __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
 template <int NP, bool SPANS>
 __global__ __launch_bounds__(kRowThreads) void k_top_fine(TopArgs a) {
     __shared__ HistShared sh;
-    __shared__ union {
-        double sum[kRowWaves];
-        DigitsShared digits;
-    } more;
+    __shared__ double sums[kRowWaves];
     const int r = blockIdx.x;
     FineRow<NP, SPANS, true> row;
     row.init((const float *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr, a.V);
-    HistOrder<FineRow<NP, SPANS, true>> order(sh, row);
+    typedef HistOrder<FineRow<NP, SPANS, true>> Order;
+    Order order(sh, row);
     uint64_t *list = (uint64_t *)sh.h;
     uint32_t n = 0;
-    if (order.template build<false>(1.0)) {
+    const auto found = order.template build<false>(1.0);
+    if (found == Order::kCounted) {
         const double part = row.run_sum ? (double)row.run_sum * exp_falling((double)row.run_max - order.weight.m) : 0.0;
         const double whole = wave_scan(part);
-        if ((threadIdx.x & 63) == 63) more.sum[threadIdx.x >> 6] = whole;
+        if ((threadIdx.x & 63) == 63) sums[threadIdx.x >> 6] = whole;
         if (order.searches()) {
             const HistPlace q = order.find_rank((uint32_t)a.k - 1);
             if (threadIdx.x == 0) {
@@ -211,14 +225,17 @@ __global__ __launch_bounds__(kRowThreads) void k_top_fine(TopArgs a) {
         __syncthreads();
         if (threadIdx.x == 0) {
             double s = 0.0;
-            for (int w = 0; w < kRowWaves; w++) s += more.sum[w];
+            for (int w = 0; w < kRowWaves; w++) s += sums[w];
             a.lse[r] = order.weight.largest() < INFINITY ? (float)(order.weight.m + log_of(s)) : INFINITY;
         }
-        const HistPlace q = sh.place;
+        HistPlace q;
+        q.pos = uniform(sh.place.pos);
+        q.above = uniform(sh.place.above);
+        q.count = uniform(sh.place.count);
         n = q.above + q.count;
-        if (n > kListRoom) {
+        if (n > kListRoom || (n < (uint32_t)a.k && row.has_lowest(sh))) {
             __syncthreads();
-            top_by_digits<0>(a, r, more.digits);
+            top_by_digits<0>(a, r, *(DigitsShared *)sh.h);
             return;
         }
         const float x_lo = bin_low(q.pos);
@@ -226,9 +243,9 @@ __global__ __launch_bounds__(kRowThreads) void k_top_fine(TopArgs a) {
             if (x >= x_lo)
                 list[atomicAdd(&sh.n_list, 1u)] = (uint64_t)~key_of_bits(__float_as_uint(x)) << 32 | (uint32_t)id;
         });
-    } else if (order.overflowed) {
+    } else if (found == Order::kByDigits) {
         __syncthreads();
-        top_by_digits<0>(a, r, more.digits);
+        top_by_digits<0>(a, r, *(DigitsShared *)sh.h);
         return;
     } else if (threadIdx.x == 0) {
         a.lse[r] = -INFINITY;
