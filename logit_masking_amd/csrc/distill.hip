@@ -17,7 +17,6 @@ namespace {
 // this (logits at a type's lowest value, say) is not used, the row is summed
 // again.
 constexpr float kSavedMax = 1024.f;
-constexpr int kPolicy = 0;
 
 struct DistillArgs {
     const void *logits;
@@ -111,9 +110,11 @@ struct Pieces {
     }
     // A piece without a usable element asks past the buffer's end, which reads
     // nothing; without a branch, so that loads stay in flight together.
+    // ONCE: nothing reads it again (the cache policy's non-temporal bit).
+    template <bool ONCE>
     __device__ __forceinline__ uint4 ask(int q, uint32_t use) const {
-        return __builtin_bit_cast(uint4,
-                                  __builtin_amdgcn_raw_buffer_load_b128(rx, use ? q * 16 : 0x7FFFFFF0, 0, kPolicy));
+        return __builtin_bit_cast(
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, use ? q * 16 : 0x7FFFFFF0, 0, ONCE ? 2 : 0));
     }
     // -inf in place of what is not usable (bfloat16: lut holds the pair
     // selects of a byte).
@@ -203,9 +204,10 @@ struct Slope {
     }
 };
 
-// One row a workgroup.  HELD pieces a thread in registers between the sum and
-// the gradient (0: the row is read again for it).
-template <int DT, int THREADS, int HELD>
+// One row a workgroup.  HELD: pieces a thread holds in registers between the
+// sum and the gradient (0: the row is read again for it).  ONCE: the sum's
+// read is the only one and large beside the caches.
+template <int DT, int THREADS, int HELD, bool ONCE>
 __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
     typedef Pieces<DT> P;
     constexpr int kWaves = THREADS / 64, kN = P::kN;
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
 #pragma unroll
             for (int i = 0; i < HELD; i++) {
                 const uint32_t b = row.usable(t + i * THREADS, use[i]);
-                d[i] = row.ask(t + i * THREADS, b);
+                d[i] = row.template ask<ONCE>(t + i * THREADS, b);
                 bytes[i / 4] = (i % 4 ? bytes[i / 4] : 0u) | b << (8 * (i % 4));
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -278,7 +280,7 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
 #pragma unroll
                 for (int i = 0; i < kAhead; i++) {
                     use[i] = row.usable(q0 + i * THREADS, use[i]);
-                    v4[i] = row.ask(q0 + i * THREADS, use[i]);
+                    v4[i] = row.template ask<ONCE>(q0 + i * THREADS, use[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < kAhead; i++) {
@@ -379,7 +381,7 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
 #pragma unroll
             for (int i = 0; i < kAhead; i++) {
                 use[i] = row.usable(q0 + i * THREADS, use[i]);
-                v4[i] = row.ask(q0 + i * THREADS, use[i]);
+                v4[i] = row.template ask<true>(q0 + i * THREADS, use[i]);
             }
 #pragma unroll
             for (int i = 0; i < kAhead; i++) {
@@ -419,27 +421,31 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
     }
 }
 
+// Which variant: both directions over up to kRowsHeld rows hold them in
+// registers while they fit (a row per CU: what counts is the time of one, and
+// a second read would add its latency); all else is read in 512 threads a
+// row, four rows a CU, where one row's sums and stores hide behind the
+// others' reads and the second read comes mostly from the memory-side cache
+// (2048 rows of 128256 bf16, both: 247 us, held 282; 24 rows of 32000 f32:
+// held 13.4 us, read twice 17).
+constexpr int kRowsHeld = 256;
+constexpr size_t kOnceBytes = size_t(32) << 20;  // a single read above this does not stay in the caches
+
 template <int DT>
 void launch_rows(const DistillArgs &a, int rows, hipStream_t st) {
     constexpr int kN = Pieces<DT>::kN;
     const int pieces = (a.V + kN - 1 + kN - 1) / kN;  // with the largest skew
     const dim3 grid(rows);
-    // both directions hold the row in registers while it fits
-    if (a.grad && !a.lse_in) {
-        if (pieces <= 4 * 1024) {
-            hipLaunchKernelGGL((k_distill_topk<DT, 1024, 4>), grid, dim3(1024), 0, st, a);
-            return;
-        }
-        if (pieces <= 8 * 1024) {
-            hipLaunchKernelGGL((k_distill_topk<DT, 1024, 8>), grid, dim3(1024), 0, st, a);
-            return;
-        }
-        if (pieces <= 16 * 1024) {
-            hipLaunchKernelGGL((k_distill_topk<DT, 1024, 16>), grid, dim3(1024), 0, st, a);
-            return;
-        }
+    const bool both = a.grad && !a.lse_in;
+    if (both && rows <= kRowsHeld && pieces <= 16 * 1024) {
+        if (pieces <= 4 * 1024) hipLaunchKernelGGL((k_distill_topk<DT, 1024, 4, false>), grid, dim3(1024), 0, st, a);
+        else if (pieces <= 8 * 1024) hipLaunchKernelGGL((k_distill_topk<DT, 1024, 8, false>), grid, dim3(1024), 0, st, a);
+        else hipLaunchKernelGGL((k_distill_topk<DT, 1024, 16, false>), grid, dim3(1024), 0, st, a);
+    } else if (!both && (size_t)rows * (size_t)a.V * Pieces<DT>::kEs > kOnceBytes) {
+        hipLaunchKernelGGL((k_distill_topk<DT, 512, 0, true>), grid, dim3(512), 0, st, a);
+    } else {
+        hipLaunchKernelGGL((k_distill_topk<DT, 512, 0, false>), grid, dim3(512), 0, st, a);
     }
-    hipLaunchKernelGGL((k_distill_topk<DT, 512, 0>), grid, dim3(512), 0, st, a);
 }
 
 }  // namespace
