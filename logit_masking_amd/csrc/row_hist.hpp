@@ -540,11 +540,12 @@ __device__ __forceinline__ void survey(HistShared &sh, bool sum_up) {
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             const int g = wave + 16 * (2 * part + i);
+            const uint32_t all = c[i].x | c[i].y | c[i].z | c[i].w;
+            if (__ballot(all != 0) == 0) continue;  // most are empty
             if (sum_up) {
                 sum = add_halves(c[i].x, add_halves(c[i].y, sum));
                 sum = add_halves(c[i].z, add_halves(c[i].w, sum));
             }
-            const uint32_t all = c[i].x | c[i].y | c[i].z | c[i].w;
             uint32_t pos = all & 0xFFFFu, neg = all >> 16;
             if (g == 0 || g == kHistDwords / 256 - 1) {  // zeros and NaNs
                 pos = neg = 0;
