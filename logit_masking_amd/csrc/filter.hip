@@ -123,8 +123,8 @@ __device__ void filter_by_digits(const FilterArgs &a, int r, SelectShared &sh) {
 
 // The place of the draw at u among what the filters keep, the pick being the
 // n-th candidate there, and the kept mass.
-template <int NP, bool SPANS>
-__device__ __forceinline__ HistPlace draw(HistOrder<HistRow<NP, SPANS>> &order, int k, float p, float mp, float u, double &mass,
+template <class ROW>
+__device__ __forceinline__ HistPlace draw(HistOrder<ROW> &order, int k, float p, float mp, float u, double &mass,
                                           uint32_t &n) {
     const int lane = threadIdx.x & 63;
     const uint32_t top = order.top_pos();
@@ -183,11 +183,11 @@ __device__ __forceinline__ HistPlace draw(HistOrder<HistRow<NP, SPANS>> &order, 
 
 // bfloat16 rows: one read, the filters on the counts of the row's values
 // (row_hist.hpp).
-template <int NP, bool SPANS>
+template <int NP, bool SPANS, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     __shared__ HistShared sh;
     const int r = blockIdx.x;
-    HistRow<NP, SPANS> row;
+    HistRow<NP, SPANS, ONCE> row;
     row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
              a.wpr, a.V);
     const float T = uniform(a.temp[r]);
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kRowThreads) void k_filter_counts(FilterArgs a) {
     const float mp = a.min_p ? uniform(a.min_p[r]) : 0.f;
     const float u = uniform(a.uniform[r]);
     const bool greedy = !(T > 0.f);
-    typedef HistOrder<HistRow<NP, SPANS>> Order;
+    typedef HistOrder<HistRow<NP, SPANS, ONCE>> Order;
     Order order(sh, row);
     const auto found = T > kEvenT ? Order::kByDigits : order.template build<true>(greedy ? 1.0 : 1.0 / (double)T);
     if (found == Order::kByDigits) {

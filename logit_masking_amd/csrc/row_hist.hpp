@@ -106,10 +106,10 @@ __device__ __forceinline__ uint32_t pos_bits(uint32_t pos) {
 __device__ __forceinline__ float bits_value(uint32_t b) { return __uint_as_float(b << 16); }
 
 // The row: NP pieces a thread held in registers; with SPANS, longer rows are
-// taken in spans of NP.  Every load is 16 bytes from a 16-byte boundary:
+// taken in spans of NP.  With ONCE the loads are non-temporal.  Every load is 16 bytes from a 16-byte boundary:
 // a row that starts past one by `skew` ids is taken from the boundary, the
 // ids before its own start never allowed.
-template <int NP, bool SPANS>
+template <int NP, bool SPANS, bool ONCE>
 struct HistRow {
     static constexpr int kSpan = NP * kPieceIds;
     static constexpr bool kExact = true;  // a position is one value
@@ -162,7 +162,7 @@ struct HistRow {
     // zeros); without a branch, so that the loads stay in flight together.
     __device__ __forceinline__ void ask(int span, int p, bool any) {
         const uint4 v = __builtin_bit_cast(
-            uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, any ? (first_id(span, p) + skew) * 2 : 0x7FFFFFF0, 0, 0));
+            uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, any ? (first_id(span, p) + skew) * 2 : 0x7FFFFFF0, 0, ONCE ? 2 : 0));
         d[p][0] = v.x; d[p][1] = v.y; d[p][2] = v.z; d[p][3] = v.w;
     }
     // Piece p's ids that are not allowed become -inf (bytes: piece p's in
@@ -828,18 +828,30 @@ struct HistOrder {
     uint32_t top_pos_;
 };
 
-// Launches KERNEL<NP, SPANS> with as many pieces as rows of V ids need (7: the
-// largest skew).  20 pieces are 80 of a thread's 128 registers; beyond that,
-// spans of 16.
-#define CG_LAUNCH_ROWS(KERNEL, V, BATCH, STREAM, ARGS)                                              \
-    do {                                                                                            \
-        const int pieces_ = ((V) + 7 + kPieceIds - 1) / kPieceIds;                                  \
-        const dim3 grid_(BATCH), block_(kRowThreads);                                               \
-        if (pieces_ <= 4) hipLaunchKernelGGL((KERNEL<4, false>), grid_, block_, 0, STREAM, ARGS);   \
-        else if (pieces_ <= 8) hipLaunchKernelGGL((KERNEL<8, false>), grid_, block_, 0, STREAM, ARGS);   \
-        else if (pieces_ <= 16) hipLaunchKernelGGL((KERNEL<16, false>), grid_, block_, 0, STREAM, ARGS); \
-        else if (pieces_ <= 20) hipLaunchKernelGGL((KERNEL<20, false>), grid_, block_, 0, STREAM, ARGS); \
-        else hipLaunchKernelGGL((KERNEL<16, true>), grid_, block_, 0, STREAM, ARGS);                \
+// Launches KERNEL<NP, SPANS, ONCE> with as many pieces as rows of V ids need
+// (7: the largest skew).  20 pieces are 80 of a thread's 128 registers; beyond
+// that, spans of 16.  ONCE for rows that are read once and do not fit the
+// caches together: above 32 MB, all L2s' size, such loads take top 64 of
+// 1024 x 151936 from 135.7 to 129.5 us and the draw of 256 x 128256 from 33.1
+// to 32.6; rows that the L2s still hold are slower so (top 20 of 128 x 128256
+// 22.5 -> 24.3 us), and so are spans, which are read again (64 x 256000
+// 35.7 -> 39.9).
+constexpr size_t kOnceBytes = size_t(32) << 20;
+#define CG_LAUNCH_PIECES(KERNEL, NP, ONCE, GRID, STREAM, ARGS)                                                \
+    do {                                                                                                      \
+        if (ONCE) hipLaunchKernelGGL((KERNEL<NP, false, true>), GRID, dim3(kRowThreads), 0, STREAM, ARGS);    \
+        else hipLaunchKernelGGL((KERNEL<NP, false, false>), GRID, dim3(kRowThreads), 0, STREAM, ARGS);        \
+    } while (0)
+#define CG_LAUNCH_ROWS(KERNEL, V, BATCH, STREAM, ARGS)                                                        \
+    do {                                                                                                      \
+        const int pieces_ = ((V) + 7 + kPieceIds - 1) / kPieceIds;                                            \
+        const bool once_ = (size_t)(BATCH) * (size_t)(V) * 2 > kOnceBytes;                                    \
+        const dim3 grid_(BATCH);                                                                              \
+        if (pieces_ <= 4) CG_LAUNCH_PIECES(KERNEL, 4, once_, grid_, STREAM, ARGS);                            \
+        else if (pieces_ <= 8) CG_LAUNCH_PIECES(KERNEL, 8, once_, grid_, STREAM, ARGS);                       \
+        else if (pieces_ <= 16) CG_LAUNCH_PIECES(KERNEL, 16, once_, grid_, STREAM, ARGS);                     \
+        else if (pieces_ <= 20) CG_LAUNCH_PIECES(KERNEL, 20, once_, grid_, STREAM, ARGS);                     \
+        else hipLaunchKernelGGL((KERNEL<16, true, false>), grid_, dim3(kRowThreads), 0, STREAM, ARGS);        \
     } while (0)
 
 }  // namespace cg

@@ -140,14 +140,14 @@ __device__ void write_top(uint64_t *list, uint32_t n, const TopArgs &a, int r, V
 
 // bfloat16 rows: one read, the k-th value from the counts (row_hist.hpp),
 // then the candidates down to it from the registers.
-template <int NP, bool SPANS>
+template <int NP, bool SPANS, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void k_top_counts(TopArgs a) {
     __shared__ HistShared sh;
     const int r = blockIdx.x;
-    HistRow<NP, SPANS> row;
+    HistRow<NP, SPANS, ONCE> row;
     row.init((const uint16_t *)a.logits + (size_t)r * (size_t)a.stride, a.mask ? a.mask + (size_t)r * a.wpr : nullptr,
              a.wpr, a.V);
-    typedef HistOrder<HistRow<NP, SPANS>> Order;
+    typedef HistOrder<HistRow<NP, SPANS, ONCE>> Order;
     Order order(sh, row);
     uint64_t *list = (uint64_t *)sh.h;
     uint32_t n = 0;
