@@ -2,14 +2,24 @@
 // workgroup.
 //
 // The counts of row_hist.hpp by the logits' upper 16 bits place every rank
-// within a few candidates and every mass within the width of a bin.  What is
-// exact comes from a window: the candidates of a range of positions, at most
-// kWindow of them, gathered and sorted with the mass of everything above them
-// summed in the same pass, one exponential per logit that counts.  A rank's
-// bin is known from the counts; a mass is looked for around where the bins'
-// middle values put it, which is nearly always right, and else further on.
-// All comes out as ranks: top-k, top-p and min-p each keep the ranks below
-// some number.
+// within its bin.  What is exact comes from a window: the candidates of whole
+// bins, at most kWindow of them, gathered and sorted.  A filter that needs the
+// row's mass, or what lies above a window that does not start at the top, has
+// one pass over the row take one exponential per candidate, into the sum and
+// into cells, one for each of the 1024 bins from the largest candidate's on:
+// their running sums say in which bin a mass is reached, and what lies above
+// every later window.  Beyond the cells (logits of ten orders of magnitude, or
+// a top below zero) a mass is looked for around where the bins' middle values
+// put it, the mass above a window summed with it, and further on where that
+// was wrong.  All comes out as ranks: top-k, top-p and min-p each keep the
+// ranks below some number.
+//
+// 64 rows of 32000, the slowest of which cuts by min-p past its 1024th rank:
+// 46 us.  Of these the read and the counts take 3, the pass with the
+// exponentials 11 (about 45 instructions each for 32 logits a thread), a
+// window 8 to 10: 3 to 4 to choose it, by one wave's searches, 3 to gather, 3
+// to sort it and sum its weights.  Before the cells every window's own pass
+// took the exponentials above it again: 57 us.
 #pragma once
 #include "row_hist.hpp"
 
@@ -155,9 +165,9 @@ struct FineRow {
         __syncthreads();
         return sh.any != 0;
     }
-    // f(x, id) for every element; what is no candidate is -inf.
+    // f(x, first id) for every four elements; what is no candidate is -inf.
     template <class F>
-    __device__ __forceinline__ void each(F f) {
+    __device__ __forceinline__ void each_four(F f) {
         const int n_spans = spans();
         for (int span = 0; span < n_spans; span++) {
             if (SPANS) load(span);
@@ -165,15 +175,25 @@ struct FineRow {
             asm volatile("" : "+v"(first));  // a caller's loop keeps nothing worked out from the ids
 #pragma unroll
             for (int p = 0; p < NP; p++) {
+                float x[4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     uint32_t w = d[p][j];
                     asm volatile("" : "+v"(w));  // (nor from the logits)
-                    f(__uint_as_float(w), first + p * kFinePieceIds + j);
+                    x[j] = __uint_as_float(w);
                 }
+                f(x, first + p * kFinePieceIds);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+    }
+    // f(x, id) for every element.
+    template <class F>
+    __device__ __forceinline__ void each(F f) {
+        each_four([&](const float (&x)[4], int first) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) f(x[j], first + j);
+        });
     }
 };
 
@@ -308,15 +328,21 @@ struct FineDraw {
     }
 
     // Chooses a window of whole bins that holds the ranks from `start` up to
-    // `end` (a bin's end): from the top if that fits, else around them; with
-    // `beyond` ranks more if there is room.  Wave 0; the result goes to fs.
-    __device__ __forceinline__ void choose(uint32_t start, uint32_t end, uint32_t last, uint32_t beyond) {
+    // `end` (a bin's end; `first` and `last` their bins): from the top if that
+    // fits, else around them, with 128 ranks before them and `beyond` behind
+    // if there is room and `sure` is not set.  Wave 0; the result goes to fs.
+    __device__ __forceinline__ void choose(uint32_t start, uint32_t end, uint32_t first, uint32_t last, uint32_t beyond, bool sure) {
         uint32_t a = key_pos(order.sh.top_key), before = 0;
         if (end > kWindow) {
-            HistPlace p = order.find_rank(start > 128 ? start - 128 : 0);
-            if (end - p.above > kWindow) p = order.find_rank(start);
-            a = p.pos;
-            before = p.above;
+            a = first;
+            before = start;
+            if (!sure) {
+                const HistPlace p = order.find_rank(start > 128 ? start - 128 : 0);
+                if (end - p.above <= kWindow) {
+                    a = p.pos;
+                    before = p.above;
+                }
+            }
         }
         const bool fits = end - before <= kWindow;
         if (fits && beyond) {
@@ -365,7 +391,10 @@ struct FineDraw {
         double base = -1.0, scale = 1.0, guess = -1.0;
         mass = -1.0;
         uint32_t from = 0, to = 65535u, key = 0, c_before = 0, c_end = 0;
-        bool masses = false, valued = false, whole = false;  // the bins have theirs; the window's bounds too; base is all
+        bool masses = false, valued = false;  // the bins have theirs; the window's bounds too
+        double total = -1.0;                  // the whole row's mass; from then on the cells hold theirs
+        const uint32_t top = key_pos(uniform(order.sh.top_key));
+        double *const cells = order.sh.cells;
         int tries = 0, stage = greedy ? kTotal : k > 0 && (uint32_t)k < count ? kTopK : kMinP;
         if (!greedy && p <= 0.f) {
             kept = 1;
@@ -394,6 +423,11 @@ struct FineDraw {
                 }
             }
             if (stage == kTotal && (greedy ? false : base >= 0.0 || (mass >= 0.0 && !(p < 1.f)))) stage = kTopP;
+            if (stage == kTotal && total >= 0.0) {
+                base = total;
+                if (mass < 0.0) mass = total;
+                stage = kTopP;
+            }
             if (stage == kTopP && (!(p < 1.f) || mass < (double)p * base)) stage = kPick;
             if (stage == kLast && kept == 0) return -1;
             const bool by_mass = stage == kTopP || stage == kPick;
@@ -444,37 +478,52 @@ struct FineDraw {
             // from the row
             if (!have) {
                 if (++tries > 24) return -1;  // (the bounds of the search keep it far from this)
-                float x_hi = -INFINITY, x_lo = INFINITY;  // the whole mass: nothing is listed
-                if (by_mass && !masses) {
+                // what is listed, x_lo .. x_hi; what is summed, above x_sum; the whole mass: nothing is listed
+                float x_hi = -INFINITY, x_lo = INFINITY, x_sum = -INFINITY;
+                bool sum_all = stage == kTotal;
+                const bool in_cells = by_mass && total >= 0.0 && reached(uniform(cells[kRowThreads - 1]));
+                if (by_mass && !in_cells && !masses) {
                     order.add_masses();
                     masses = true;
-                    if (whole) {
+                    if (total >= 0.0) {
                         if (order.searches()) {
                             const double m = order.total_mass();
                             if (t == 0) fs.value[0] = m;
                         }
                         __syncthreads();
-                        scale = base / uniform(fs.value[0]);
+                        scale = total / uniform(fs.value[0]);
                         __syncthreads();
                     }
                 }
                 if (stage != kTotal) {
                     if (!(guess >= 0.0)) guess = target / scale;
                     __syncthreads();
+                    if (in_cells) {
+                        if (reached(cells[t]) && !(t && reached(cells[t - 1]))) fs.hit = (int)t;
+                        __syncthreads();
+                    }
                     if (t < 64) {
                         if (stage == kMinP) {
                             const HistPlace q = order.find_rank(c_end > c_before ? c_end - 1 : c_before - 1);
-                            choose(c_before ? c_before - 1 : 0, q.above + q.count, q.pos, 0);
+                            const HistPlace q0 = q.above < c_before ? q : order.find_rank(c_before ? c_before - 1 : 0);
+                            choose(q0.above, q.above + q.count, q0.pos, q.pos, 0, true);
                         } else {
                             HistPlace q;
-                            if (by_mass) {
+                            if (in_cells) {
+                                const uint32_t pos = min(max(top + (uint32_t)fs.hit, from), to);
+                                q.pos = pos;
+                                q.above = pos ? order.count_to(pos - 1) : 0u;
+                                q.count = uniform(bin_count(pos));
+                                if (!q.count) q = order.find_rank(q.above);  // (a bound of the search, not a cell)
+                            } else if (by_mass) {
                                 q = stage == kTopP ? order.template find<2>(0, guess) : order.template find<1>(0, guess);
                                 if (q.pos < from) q = order.find_rank(order.count_to(from - 1));
                                 else if (q.pos > to) q = order.find_rank(order.count_to(to) - 1);
                             } else {
                                 q = order.find_rank(rank);
                             }
-                            choose(q.above, q.above + q.count, q.pos, by_mass ? 64 + (q.above + q.count) / 8 : 0);
+                            choose(q.above, q.above + q.count, q.pos, q.pos, by_mass && !in_cells ? 64 + (q.above + q.count) / 8 : 0,
+                                   !by_mass || in_cells);
                         }
                     }
                     __syncthreads();
@@ -484,27 +533,75 @@ struct FineDraw {
                     above = uniform(fs.above);
                     x_hi = bin_high(lo);
                     x_lo = bin_low(hi);
+                    sum_all = above && total < 0.0;
+                    if (!sum_all) x_sum = x_hi;
+                }
+                const bool to_cells = sum_all && !greedy, sums = sum_all || (above && lo - top > kRowThreads);
+                if (to_cells) {
+                    cells[t] = 0.0;
+                    __syncthreads();
                 }
                 double s = 0.0;
-                order.row.each([&](float x, int id) {
-                    if (x > x_hi) {
-                        s += order.weight(x);
-                    } else if (x >= x_lo) {
-                        const uint32_t at = atomicAdd(&fs.n, 1u);
-                        if (at < kWindow) fs.list[at] = (uint64_t)~key_of_bits(__float_as_uint(x)) << 32 | (uint32_t)id;
+                order.row.each_four([&](const float (&x)[4], int first) {
+                    if (sums) {
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            if (!(x[j] > x_sum)) continue;
+                            const double w = order.weight(x[j]);
+                            s += w;
+                            if (to_cells) {
+                                // in units of 2^-41, so that the order of the sums is all one
+                                const uint32_t cell = key_pos(key_of_bits(__float_as_uint(x[j]))) - top;
+                                if (cell < kRowThreads)
+                                    atomicAdd((unsigned long long *)&cells[cell],
+                                              (unsigned long long)(__double_as_longlong(w + 2048.0) - __double_as_longlong(2048.0)));
+                            }
+                        }
+                    }
+                    if (!sum_all) {
+                        // one addition to the list's length a wave: its answer takes 100 instructions' time
+                        uint64_t in[4];
+                        uint32_t found = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            in[j] = __ballot(x[j] >= x_lo && x[j] <= x_hi);
+                            found += (uint32_t)__popcll(in[j]);
+                        }
+                        if (found) {
+                            uint32_t at = 0;
+                            if ((t & 63) == 0) at = atomicAdd(&fs.n, found);
+                            at = uniform(at);
+#pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                const uint32_t slot = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(in[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in[j], 0u));
+                                if (x[j] >= x_lo && x[j] <= x_hi && slot < kWindow)
+                                    fs.list[slot] = (uint64_t)~key_of_bits(__float_as_uint(x[j])) << 32 | (uint32_t)(first + j);
+                                at += (uint32_t)__popcll(in[j]);
+                            }
+                        }
                     }
                 });
                 s = block_sum(s);
-                if (stage == kTotal) {
-                    base = s;
-                    whole = true;
-                    if (mass < 0.0) mass = s;
-                    if (greedy) kept = 1;
-                    stage = greedy ? kLast : kTopP;
-                    tries = 0;
+                if (to_cells) {
+                    total = s;
+                    const double m = wave_scan((double)(uint64_t)__double_as_longlong(cells[t]) * 0x1p-41);
+                    if ((t & 63) == 63) fs.wave[t >> 6] = m;
+                    __syncthreads();
+                    double before = 0.0;
+#pragma unroll 1
+                    for (uint32_t v = 0; v < t >> 6; v++) before += fs.wave[v];
+                    cells[t] = before + m;
+                    n = 0;  // (a window may have been chosen, but was not listed)
+                    __syncthreads();
                     continue;
                 }
-                mass_above = s;
+                if (greedy && stage == kTotal) {
+                    mass = s;
+                    kept = 1;
+                    stage = kLast;
+                    continue;
+                }
+                mass_above = above && lo - top <= kRowThreads ? uniform(cells[lo - top - 1]) : s;
                 n = min(uniform(fs.n), kWindow);
                 sort_window(lo, hi, n);
                 const double w = t < n ? order.weight(value_of_key(~(uint32_t)(fs.list[t] >> 32))) : 0.0;
@@ -515,8 +612,8 @@ struct FineDraw {
 #pragma unroll 1
                 for (uint32_t v = 0; v < t >> 6; v++) before += fs.wave[v];
                 fs.mass[t] = before + m;
-                valued = by_mass;
-                if (by_mass && t < 64) {  // the bounds' mass by the bins, for another try
+                valued = by_mass && !in_cells;
+                if (valued && t < 64) {  // the bounds' mass by the bins, for another try
                     const double m0 = lo ? order.mass_to(lo - 1) : 0.0, m1 = order.mass_to(hi);
                     if (t == 0) {
                         fs.value[0] = m0;

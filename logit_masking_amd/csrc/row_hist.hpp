@@ -43,7 +43,13 @@ struct HistPlace {
 struct HistShared {
     uint32_t h[kHistDwords];
     uint32_t dummy[64];  // where lanes count what is no candidate
-    uint4 lut[256];      // mask byte -> half of ones per allowed id of four pairs
+    union {
+        struct {
+            uint4 lut[256];              // mask byte -> half of ones per allowed id of four pairs
+            uint32_t list[kRowThreads];  // candidates of a value by piece and wave
+        };
+        double cells[kRowThreads];  // (rows of float32: row_fine.hpp)
+    };
     uint32_t blk_cnt[kHistBlocks];
     double blk_mass[kHistBlocks];
     uint32_t counted;    // sum of every count, the dummies' included
@@ -52,7 +58,6 @@ struct HistShared {
     uint32_t top_key;    // key of the largest candidate (rows of float32)
     uint32_t n_blocks;   // blocks with a candidate, listed in any order
     uint16_t blocks[kHistBlocks];
-    uint32_t list[kRowThreads];
     uint32_t n_list;
     uint32_t w_cnt[kRowWaves];
     int found;
