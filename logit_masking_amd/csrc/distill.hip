@@ -32,6 +32,7 @@ struct DistillArgs {
     const float *weight;
     void *grad;
     int64_t grad_stride;
+    int span;  // pieces of a row that one workgroup writes the gradient of
 };
 
 // ---- single elements ----------------------------------------------------------
@@ -54,17 +55,27 @@ __device__ __forceinline__ void store_x(void *p, size_t i, float v) {
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-template <int WAVES, class T, class F>
-__device__ T block_reduce(T v, T *slots, F op) {
+// Reduces N numbers a thread over the workgroup.
+template <int WAVES, int N, class T, class F>
+__device__ void block_reduce(T (&v)[N], T *slots, F op) {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) v = op(v, __shfl_xor(v, d));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = slots[threadIdx.x & (WAVES - 1)];
+    for (int d = 32; d; d >>= 1) {
 #pragma unroll
-    for (int d = WAVES / 2; d; d >>= 1) v = op(v, __shfl_xor(v, d));
-    return v;
+        for (int n = 0; n < N; n++) v[n] = op(v[n], __shfl_xor(v[n], d));
+    }
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int n = 0; n < N; n++) slots[n * WAVES + (threadIdx.x >> 6)] = v[n];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; n++) v[n] = slots[n * WAVES + (threadIdx.x & (WAVES - 1))];
+#pragma unroll
+    for (int d = WAVES / 2; d; d >>= 1) {
+#pragma unroll
+        for (int n = 0; n < N; n++) v[n] = op(v[n], __shfl_xor(v[n], d));
+    }
 }
 
 // ---- the row in 16-byte pieces ------------------------------------------------
@@ -213,8 +224,8 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
     constexpr int kWaves = THREADS / 64, kN = P::kN;
     constexpr int kEntries = (CG_MAX_TOP + THREADS - 1) / THREADS;  // teacher entries a thread
     constexpr int kAhead = 4;                                      // pieces a thread asks for together
-    __shared__ double dslots[kWaves];
-    __shared__ float fslots[kWaves];
+    __shared__ double dslots[2 * kWaves];
+    __shared__ float fslots[2 * kWaves];
     __shared__ float p_of[CG_MAX_TOP];
     __shared__ int id_of[CG_MAX_TOP];
     __shared__ uint4 lut[DT == 1 ? 256 : 1];
@@ -224,9 +235,30 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
     char *g = a.grad ? (char *)a.grad + (size_t)r * (size_t)a.grad_stride * P::kEs : nullptr;
     const P row(x, mask, g, a.V);
     const int n_pieces = row.count();
+    const int from = HELD ? 0 : blockIdx.y * a.span, upto = HELD ? n_pieces : min(n_pieces, from + a.span);
     auto fmax_op = [](float p, float q) { return fmaxf(p, q); };
     auto sum_op = [](double p, double q) { return p + q; };
     const float kk = (float)(1.4426950408889634 / (double)a.tau);
+
+    // the teacher's entries, asked for before the row: three reads one after the other
+    int id[kEntries];
+    float s_id[kEntries], tl[kEntries];
+    double p[kEntries];
+    float tmax = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kEntries; i++) {
+        const int e = t + i * THREADS;
+        id[i] = -1;
+        s_id[i] = tl[i] = -INFINITY;
+        if (e < a.k) {
+            id[i] = a.t_ids[(size_t)r * a.k + e];
+            if (id[i] >= 0 && id[i] < a.V) {
+                if (!mask || ((mask[id[i] >> 6] >> (id[i] & 63)) & 1)) s_id[i] = load_x<DT>(x, id[i]);
+                if (s_id[i] != -INFINITY) tl[i] = a.t_logits[(size_t)r * a.k + e];
+            }
+        }
+        tmax = fmaxf(tmax, tl[i]);
+    }
     if (DT == 1) {
         for (int v = t; v < 256; v += THREADS) {
             uint32_t m[4];
@@ -240,15 +272,13 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
 
     // the normaliser: L = m / tau + ln sum 2^((x - m) kk), kept apart as m and
     // log2 of the sum; a saved one stands for a sum of 1 at m = 0
-    double L, ln_sum = 0.0;
-    float base = 0.f, l2s;
     const float saved = a.lse_in ? a.lse_in[r] : INFINITY;
+    const bool is_saved = HELD == 0 && fabsf(saved) <= kSavedMax;
+    double L = (double)saved, ln_sum = 0.0;
+    float base = 0.f, l2s = (float)(L * 1.4426950408889634);
     uint4 d[HELD ? HELD : 1];
-    if (HELD == 0 && fabsf(saved) <= kSavedMax) {
-        L = (double)saved;
-        l2s = (float)(L * 1.4426950408889634);
-    } else {
-        Running run{-INFINITY, 0.f};
+    Running run{-INFINITY, 0.f};
+    if (!is_saved) {
         if (HELD) {
             uint32_t use[HELD ? HELD : 1], bytes[(HELD + 3) / 4 + 1];  // four pieces' bits a word
 #pragma unroll
@@ -292,45 +322,30 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
                 }
             }
         }
-        const float best = block_reduce<kWaves>(run.m, fslots, fmax_op);
-        // (a thread that saw only -inf, or a NaN beside nothing else, has no maximum to scale from)
-        const double part = run.m == best ? (double)run.s : run.s == 0.f ? 0.0 : (double)run.s * exp_falling(((double)run.m - (double)best) / (double)a.tau);
-        const double sum = block_reduce<kWaves>(part, dslots, sum_op);
-        ln_sum = log_of(sum);
-        L = (double)best / (double)a.tau + ln_sum;
-        base = best;
-        l2s = (float)(ln_sum * 1.4426950408889634);
     }
 
-    // the teacher's distribution over the entries the student can take
-    int id[kEntries];
-    float s_id[kEntries], tl[kEntries];
-    double p[kEntries];
-    float tmax = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kEntries; i++) {
-        const int e = t + i * THREADS;
-        id[i] = -1;
-        s_id[i] = tl[i] = -INFINITY;
-        if (e < a.k) {
-            id[i] = a.t_ids[(size_t)r * a.k + e];
-            if (id[i] >= 0 && id[i] < a.V) {
-                if (!mask || ((mask[id[i] >> 6] >> (id[i] & 63)) & 1)) s_id[i] = load_x<DT>(x, id[i]);
-                if (s_id[i] != -INFINITY) tl[i] = a.t_logits[(size_t)r * a.k + e];
-            }
-        }
-        tmax = fmaxf(tmax, tl[i]);
-    }
-    tmax = block_reduce<kWaves>(tmax, fslots, fmax_op);
+    // both maxima, then both sums: the row's, and that of the teacher's
+    // distribution over the entries the student can take
+    float most[2] = {run.m, tmax};
+    block_reduce<kWaves>(most, fslots, fmax_op);
+    tmax = most[1];
     const bool some = tmax > -INFINITY;
-    double esum = 0.0;
+    // (a thread that saw only -inf, or a NaN beside nothing else, has no maximum to scale from)
+    double sum[2] = {run.m == most[0] ? (double)run.s : run.s == 0.f ? 0.0 : (double)run.s * exp_falling(((double)run.m - (double)most[0]) / (double)a.tau),
+                     0.0};
 #pragma unroll
     for (int i = 0; i < kEntries; i++) {
         p[i] = tl[i] > -INFINITY ? exp_falling(((double)tl[i] - (double)tmax) / (double)a.tau) : 0.0;
-        esum += p[i];
+        sum[1] += p[i];
     }
-    esum = block_reduce<kWaves>(esum, dslots, sum_op);
-    const double ln_esum = log_of(esum);
+    block_reduce<kWaves>(sum, dslots, sum_op);
+    const double esum = sum[1], ln_esum = log_of(esum);
+    if (!is_saved) {
+        ln_sum = log_of(sum[0]);
+        L = (double)most[0] / (double)a.tau + ln_sum;
+        base = most[0];
+        l2s = (float)(ln_sum * 1.4426950408889634);
+    }
     double loss = 0.0;
 #pragma unroll
     for (int i = 0; i < kEntries; i++) {
@@ -340,8 +355,9 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
                             ln_sum);
     }
     if (a.loss) {
-        loss = block_reduce<kWaves>(loss, dslots, sum_op);
-        if (t == 0) a.loss[r] = (float)((double)a.tau * (double)a.tau * loss);
+        double whole[1] = {loss};
+        block_reduce<kWaves>(whole, dslots, sum_op);
+        if (t == 0) a.loss[r] = (float)((double)a.tau * (double)a.tau * whole[0]);
     }
     if (a.lse && t == 0) a.lse[r] = (float)L;
     if (!g) return;
@@ -357,7 +373,7 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
         row.put(q, z);
     };
     if (!some) {  // nothing recorded, or nothing allowed
-        for (int q = t; q < n_pieces; q += THREADS) zeros(q);
+        for (int q = from + t; q < upto; q += THREADS) zeros(q);
         return;
     }
     if (HELD) {
@@ -373,7 +389,7 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
             __builtin_amdgcn_sched_barrier(0);
         }
     } else {
-        for (int q0 = t; q0 < n_pieces; q0 += kAhead * THREADS) {
+        for (int q0 = from + t; q0 < upto; q0 += kAhead * THREADS) {
             uint32_t use[kAhead];
             uint4 v4[kAhead];
 #pragma unroll
@@ -386,7 +402,7 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
 #pragma unroll
             for (int i = 0; i < kAhead; i++) {
                 const int q = q0 + i * THREADS;
-                if (q >= n_pieces) continue;
+                if (q >= upto) continue;
                 if (!__any(use[i] != 0)) {
                     zeros(q);
                     continue;
@@ -399,7 +415,7 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
             }
         }
     }
-    // then the entries' places, over what was just written
+    // then the entries' places here, over what was just written
 #pragma unroll
     for (int i = 0; i < kEntries; i++) {
         const int e = t + i * THREADS;
@@ -411,12 +427,13 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
     __syncthreads();  // the row's stores are done as well
 #pragma unroll
     for (int i = 0; i < kEntries; i++) {
-        if (p[i] > 0.0) {
-            double sum = 0.0;
-            for (int j = 0; j < a.k; j++) sum += id_of[j] == id[i] ? (double)p_of[j] : 0.0;
-            const double y = ((double)s_id[i] - (double)base) / (double)a.tau - (HELD == 0 && fabsf(saved) <= kSavedMax ? L : ln_sum);
+        const int piece = (id[i] + row.skew) / kN;
+        if (p[i] > 0.0 && piece >= from && piece < upto) {
+            double own = 0.0;
+            for (int j = 0; j < a.k; j++) own += id_of[j] == id[i] ? (double)p_of[j] : 0.0;
+            const double y = ((double)s_id[i] - (double)base) / (double)a.tau - (is_saved ? L : ln_sum);
             const double q = y == y ? exp_falling(y) : y;
-            store_x<DT>(g, id[i], (float)((q - sum) * scale));
+            store_x<DT>(g, id[i], (float)((q - own) * scale));
         }
     }
 }
@@ -431,11 +448,23 @@ __global__ __launch_bounds__(THREADS) void k_distill_topk(DistillArgs a) {
 constexpr int kRowsHeld = 256;
 constexpr size_t kOnceBytes = size_t(32) << 20;  // a single read above this does not stay in the caches
 
+// The gradient from saved normalisers needs no sum of the row, so that several
+// workgroups share one until there are two a CU, each with a load in flight a
+// thread at least: 24 rows of 32000 f32 15.9 -> 10.9 us, 64 of 50021 22.2 ->
+// 12.5, 200 of 50021 26.1 -> 24.8; up to eight a CU take 1024 of 128256 bf16
+// from 114.4 to 116.6.  Not in place, where one would overwrite logits that
+// another still looks up for the teacher's ids.
+constexpr int kGradGroups = 512, kGradPieces = 4 * 512;
+
 template <int DT>
-void launch_rows(const DistillArgs &a, int rows, hipStream_t st) {
+void launch_rows(DistillArgs a, int rows, hipStream_t st) {
     constexpr int kN = Pieces<DT>::kN;
     const int pieces = (a.V + kN - 1 + kN - 1) / kN;  // with the largest skew
-    const dim3 grid(rows);
+    int parts = 1;
+    if (a.lse_in && (const void *)a.grad != a.logits)
+        parts = std::max(1, std::min((kGradGroups + rows - 1) / rows, (pieces + kGradPieces - 1) / kGradPieces));
+    a.span = (pieces + parts - 1) / parts;
+    const dim3 grid(rows, parts);
     const bool both = a.grad && !a.lse_in;
     if (both && rows <= kRowsHeld && pieces <= 16 * 1024) {
         if (pieces <= 4 * 1024) hipLaunchKernelGGL((k_distill_topk<DT, 1024, 4, false>), grid, dim3(1024), 0, st, a);
@@ -482,7 +511,7 @@ int cg_distill_topk(const void *d_logits, int32_t dtype, int32_t rows, int32_t v
                     const float *d_weight, void *d_out_grad, int64_t grad_stride, void *stream) {
     if (rows > 0 && !d_out_loss) return distill_arg_error("NULL device pointer");
     const DistillArgs a{d_logits, row_stride, d_mask,     words_per_row, vocab,    d_teacher_ids, d_teacher_logits, k,
-                        temperature, nullptr, d_out_loss, d_out_lse,     d_weight, d_out_grad,    grad_stride};
+                        temperature, nullptr, d_out_loss, d_out_lse,     d_weight, d_out_grad,    grad_stride, 0};
     return distill_launch(a, dtype, rows, stream);
 }
 
@@ -492,7 +521,7 @@ int cg_distill_topk_grad(const void *d_logits, int32_t dtype, int32_t rows, int3
                          const float *d_weight, void *d_out_grad, int64_t grad_stride, void *stream) {
     if (rows > 0 && (!d_lse || !d_out_grad)) return distill_arg_error("NULL device pointer");
     const DistillArgs a{d_logits, row_stride, d_mask,  words_per_row, vocab,    d_teacher_ids, d_teacher_logits, k,
-                        temperature, d_lse,   nullptr, nullptr,       d_weight, d_out_grad,    grad_stride};
+                        temperature, d_lse,   nullptr, nullptr,       d_weight, d_out_grad,    grad_stride, 0};
     return distill_launch(a, dtype, rows, stream);
 }
 

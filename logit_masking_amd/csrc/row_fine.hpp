@@ -8,10 +8,9 @@
 // one pass over the row take one exponential per candidate, into the sum and
 // into cells, one for each of the 1024 bins from the largest candidate's on:
 // their running sums say in which bin a mass is reached, and what lies above
-// every later window.  Beyond the cells (logits of ten orders of magnitude, or
-// a top below zero) a mass is looked for around where the bins' middle values
-// put it, the mass above a window summed with it, and further on where that
-// was wrong.  All comes out as ranks: top-k, top-p and min-p each keep the
+// every later window.  Beyond the cells (eight powers of two from the largest
+// logit) a mass is looked for around where the bins' middle values put it, the
+// mass above a window summed with it, and further on where that was wrong.  All comes out as ranks: top-k, top-p and min-p each keep the
 // ranks below some number.
 //
 // 64 rows of 32000, the slowest of which cuts by min-p past its 1024th rank:

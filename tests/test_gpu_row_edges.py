@@ -195,6 +195,24 @@ def test_rows_far_apart(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("way", ["both", "grad"])
+def test_gradient_in_place(way, dtype):
+    """The gradient over the student's logits, of few long rows and of more than a row per unit."""
+    say("gradient in place", way, dtype)
+    rng = np.random.default_rng(13)
+    for B, V in ((2, 131075), (5, 50021), (300, 9000)):
+        x = F.make(rng, B, V, dtype)
+        allowed = F.masks(rng, B, V)
+        ids, t = D.teacher(rng, x, None, 40, V)
+        w = rng.uniform(0.1, 2, B).astype(np.float32)
+        xs = x.double().cpu().numpy()
+        apart = D.run(x, F.pack(allowed), ids, t, 1.5, way, w)
+        D.check(xs, allowed, ids, t, 1.5, w, apart, dtype, way == "grad")
+        same = D.run(x, F.pack(allowed), ids, t, 1.5, way, w, inplace=True)
+        assert all(np.array_equal(a, b) for a, b in zip(apart, same))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_two_streams_at_once(dtype):
     """Calls that run beside each other, on rows and outputs of their own, give what they give alone."""
     import torch
