@@ -374,7 +374,7 @@ size_t cg_filter_workspace_bytes(int32_t batch, int32_t vocab);
  * equal logits (the two zeros are equal) by rising id.  With T =
  * d_temperature[r] > 0 and m the largest candidate logit, a candidate's
  * weight is w = exp((x - m) / T) (1 where x = m, so a logit of +inf takes
- * all), computed in 64 bits and held in units of 2^-40.  In this order:
+ * all), computed in 64 bits to 2^-40 of the largest.  In this order:
  *   top-k   ranks below k = d_top_k[r] stay (k <= 0: all);
  *   top-p   rank j > 0 stays while the weight before it is less than
  *           d_top_p[r] times the weight top-k left (>= 1 or NaN: all,
@@ -406,7 +406,8 @@ size_t cg_top_workspace_bytes(int32_t batch, int32_t vocab, int32_t k);
  * The first k ranks of each row's candidates (the order of
  * cg_filter_sample): d_out_ids[r * k + j] int32 and d_out_logits[r * k + j]
  * float32 (the logit as it is), -1 and -inf past the last candidate, and
- * d_out_lse[r] = ln sum exp(x) over all candidates (-inf without one), so
+ * d_out_lse[r] = ln sum exp(x) over all candidates (-inf without one, +inf
+ * with a logit of +inf), so
  * that logit - lse is a token's log-probability under the mask: the record a
  * student is trained on (cg_distill_topk) and the top log-probabilities of a
  * reply.  1 <= k <= CG_MAX_TOP.  d_workspace: cg_top_workspace_bytes(batch,
@@ -430,8 +431,8 @@ int cg_top_logits(const void *d_logits, int32_t dtype, int32_t batch, int32_t vo
  *   d loss / d x_v = tau (q_v - sum of p_j with id_j = v) where v is
  *   allowed, exactly 0 elsewhere.
  * A row without an entry (a padded position, an empty mask) has loss 0 and
- * gradient 0.  An allowed NaN makes the row's loss, normaliser and gradient
- * NaN; masked logits may hold anything.
+ * gradient 0.  An allowed NaN or +inf makes the row's loss, normaliser and
+ * gradient NaN; masked logits may hold anything.
  *   d_out_loss[rows]; d_out_lse[rows] = L (may be NULL; -inf for an empty
  *   row), float32;
  *   d_out_grad: NULL, or rows grad_stride elements apart in the logits'
@@ -439,7 +440,7 @@ int cg_top_logits(const void *d_logits, int32_t dtype, int32_t batch, int32_t vo
  *   the derivative of the caller's objective by each row's loss), elements
  *   past vocab left untouched.  It may be d_logits itself with the same
  *   stride; otherwise they must not overlap.
- * temperature = tau, positive and finite; 1 <= k <= CG_MAX_TOP.
+ * temperature = tau, 1e-30 to 1e30; 1 <= k <= CG_MAX_TOP.
  */
 int cg_distill_topk(const void *d_logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
                     const uint64_t *d_mask, int32_t words_per_row, const int32_t *d_teacher_ids,
@@ -447,7 +448,8 @@ int cg_distill_topk(const void *d_logits, int32_t dtype, int32_t rows, int32_t v
                     const float *d_weight, void *d_out_grad, int64_t grad_stride, void *stream);
 
 /* The gradient of cg_distill_topk alone: d_lse[rows] is that call's
- * d_out_lse for the same logits, mask and temperature. */
+ * d_out_lse for the same logits, mask and temperature.  A normaliser above
+ * 1024 in size, which float32 holds too coarsely, is summed again. */
 int cg_distill_topk_grad(const void *d_logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
                          const uint64_t *d_mask, int32_t words_per_row, const int32_t *d_teacher_ids,
                          const float *d_teacher_logits, int32_t k, float temperature, const float *d_lse,

@@ -672,6 +672,9 @@ def _grad_arg(grad, logits, B, V):
     a, b = grad.data_ptr(), logits.data_ptr()
     if a != b or stride != (max(logits.stride(0), V) if B == 1 else logits.stride(0)):
         size = logits.element_size()
+        at = (a - b) // size % stride  # rows that lie between the logits' rows
+        if logits.stride(0) == stride and V <= at <= stride - V:
+            return a, stride
         if B and a < b + ((B - 1) * logits.stride(0) + V) * size and b < a + ((B - 1) * stride + V) * size:
             raise ValueError("out_grad overlaps the logits (it may only be the same rows)")
     return a, stride
@@ -747,6 +750,9 @@ def distill_topk_loss(logits, teacher_ids, teacher_logits, mask=None, temperatur
     logits: logits [..., >= vocab], teacher_ids and teacher_logits [..., k],
     mask [..., W] or None; float32 losses of the leading shape."""
     lead = logits.shape[:-1]
+    for t, n in ((teacher_ids, "teacher_ids"), (teacher_logits, "teacher_logits"), (mask, "mask")):
+        if t is not None and t.shape[:-1] != lead:
+            raise ValueError(f"{n} must have the logits' leading shape")
     x = logits.reshape(-1, logits.shape[-1])
     if x.stride(-1) != 1:
         x = x.contiguous()
@@ -754,8 +760,4 @@ def distill_topk_loss(logits, teacher_ids, teacher_logits, mask=None, temperatur
     top = teacher_logits.reshape(-1, teacher_logits.shape[-1]).contiguous()
     if mask is not None:
         mask = mask.reshape(-1, mask.shape[-1]).contiguous()
-    for t, n in ((teacher_ids, "teacher_ids"), (teacher_logits, "teacher_logits")) + \
-            (((mask, "mask"),) if mask is not None else ()):
-        if t.reshape(-1, t.shape[-1]).shape[0] != x.shape[0]:
-            raise ValueError(f"{n} must have the logits' leading shape")
     return _distill_function().apply(x, mask, ids, top, temperature, vocab).reshape(lead)

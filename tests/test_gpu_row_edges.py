@@ -275,6 +275,80 @@ def test_mask_bits_past_the_vocabulary(dtype):
                 D.run(wide, ones, ids, t, 1.0, "both", s[0], vocab=V), dtype)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_rows_between_the_logits_rows(dtype):
+    """One tensor holds each row's logits and, behind them, its gradient."""
+    import torch
+    say("gradient between", dtype)
+    rng = np.random.default_rng(15)
+    B, V = 6, 2003
+    both = torch.zeros((B, 2 * V + 3), dtype=getattr(torch, dtype), device="cuda")
+    x, g = both[:, :V], both[:, V:2 * V]
+    x.copy_(F.make(rng, B, V, dtype))
+    kept = x.clone()
+    ids, t = D.teacher(rng, x, None, 8, V)
+    i, t2 = torch.from_numpy(ids).cuda(), torch.from_numpy(t).cuda()
+    w = torch.full((B,), 0.75, device="cuda")
+    loss, lse = torch.empty(B, device="cuda"), torch.empty(B, device="cuda")
+    cg.distill_topk(x, None, i, t2, 2.0, loss, lse, weight=w, out_grad=g)
+    want = torch.empty((B, V), dtype=x.dtype, device="cuda")
+    cg.distill_topk(kept, None, i, t2, 2.0, loss, lse, weight=w, out_grad=want)
+    torch.cuda.synchronize()
+    assert torch.equal(x, kept) and torch.equal(g, want) and not both[:, 2 * V:].any()
+    with pytest.raises(ValueError, match="overlap"):
+        cg.distill_topk(x, None, i, t2, 2.0, loss, lse, weight=w, out_grad=both[:, V - 1:2 * V - 1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_temperatures_at_their_ends(dtype):
+    """Distillation at the smallest and largest temperatures: all on the largest logit, and all alike."""
+    import torch
+    say("distill temperatures", dtype)
+    rng = np.random.default_rng(16)
+    B, V, k = 4, 1500, 6
+    x = F.make(rng, B, V, dtype)
+    ids, t = D.teacher(rng, x, None, k, V)
+    w = np.full(B, 1.0, dtype=np.float32)
+    xs = x.double().cpu().numpy()
+    for tau in (1e-30, 1e30):
+        loss, lse, grad = D.run(x, None, ids, t, tau, "both", w)
+        assert np.isfinite(grad).all()
+        if tau > 1:  # q = 1 / V everywhere, p alike over a row's entries: tau (q - p) to float32's precision
+            assert np.abs(lse - math.log(V)).max() <= 2.0 ** -24 * (math.log(V) + 6) + 1e-6
+        else:
+            assert np.allclose(lse, xs.max(1) / float(np.float32(tau)), rtol=2.0 ** -23)
+            # w tau (q - p) of the largest logit's id: within tau of nothing, and nothing anywhere else but at entries
+            rest = xs < xs.max(1, keepdims=True)
+            for r in range(B):
+                rest[r, ids[r][(ids[r] >= 0) & (ids[r] < V)]] = False
+            assert not grad[rest].any() and np.abs(grad).max() <= 1.01e-30
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("value", [INF, math.nan])
+def test_distillation_of_what_is_no_number(value, dtype):
+    """An allowed NaN or +inf spreads over its row's allowed places, in every variant, and over no other row."""
+    import torch
+    say("no number", value, dtype)
+    rng = np.random.default_rng(17)
+    for B, V in ((3, 900), (300, 2500), (2, 70001)):
+        x = F.make(rng, B, V, dtype)
+        allowed = rng.random((B, V)) < 0.7
+        ids, t = D.teacher(rng, x, None, 6, V)
+        allowed[1, ids[1, 0]] = True  # an entry that the student can take
+        w = np.ones(B, dtype=np.float32)
+        at = int(np.flatnonzero(allowed[1])[5])
+        for way in ("both", "grad"):
+            clean = D.run(x, F.pack(allowed), ids, t, 1.0, way, w)
+            y = x.clone()
+            y[1, at] = value
+            loss, lse, grad = D.run(y, F.pack(allowed), ids, t, 1.0, way, w)
+            assert math.isnan(loss[1]) and math.isnan(lse[1])
+            assert np.isnan(grad[1][allowed[1]]).all() and not grad[1][~allowed[1]].any()
+            rest = np.arange(B) != 1
+            assert all(np.array_equal(a[rest], b[rest]) for a, b in zip((loss, lse, grad), clean))
+
+
 def test_rows_that_share_storage_are_refused():
     import torch
     say("shared rows")

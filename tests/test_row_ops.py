@@ -61,6 +61,22 @@ def test_c_refusals(call, how):
     assert _err()
 
 
+@pytest.mark.parametrize("tau", [1e-31, 1e-45, 1.1e30])
+def test_temperatures_whose_inverse_is_no_float32(tau):
+    for call in (_distill, _grad):
+        assert call(tau=tau) == cg.CG_E_ARG
+        assert "temperature" in _err()
+
+
+def test_loss_refuses_other_leading_shapes():
+    import torch
+    x, i, t = torch.zeros(2, 3, 50), torch.zeros(2, 3, 4, dtype=torch.int32), torch.zeros(2, 3, 4)
+    m = torch.zeros(2, 3, 1, dtype=torch.int64)
+    for args in ((x, i[:1], t, m), (x, i, t.reshape(6, 4), m), (x, i, t, m[:, :2]), (x, i.reshape(3, 2, 4), t.reshape(3, 2, 4), None)):
+        with pytest.raises(ValueError, match="leading shape"):
+            cg.distill_topk_loss(*args)
+
+
 def test_empty_batches_do_nothing():
     """No rows: CG_OK without touching a pointer; the sizes are still checked."""
     assert _sample(batch=0, ptrs=(None,) * 5, ids=None, lp=None) == cg.CG_OK
