@@ -192,11 +192,11 @@ __device__ __forceinline__ HistPlace draw(HistOrder<ROW> &order, int k, float p,
 // bfloat16 rows: one read, the filters on the counts of the row's values
 // (row_hist.hpp).
 //
-// 256 rows of 128256 under a third-full mask, one per CU: 33 us, of which the
-// loads and counts take 14 (30 MB read: 2.1 TB/s meanwhile; the LDS takes an
-// addition a logit), finding the blocks in use 2, their masses 2, the searches
-// by one wave 3, the id 5, launch and end 4.  512 rows of 256000 in two spans:
-// 104 us, the first 24 of each row's 48 at 5.5 TB/s.  A workgroup holds 143 of
+// 256 rows of 128256 under a grammar's mask, one per CU: 33 us, of which the
+// loads and counts take 14 (62 MB: 4.4 TB/s meanwhile; an addition in LDS a
+// logit), finding the blocks in use 2, their masses 2, the searches by one
+// wave 3, the id 5, launch and end 4.  512 rows of 256000 in two spans:
+// 104 us, 24 of each row's 48 for the loads and counts, at 5.5 TB/s.  A workgroup holds 143 of
 // a CU's 160 KB of LDS, so that a row's searches have no other row's loads
 // beside them; counts that leave room for two would hold a row's 65536 values
 // in fewer than 16 bits each.

@@ -144,7 +144,7 @@ __device__ void write_top(uint64_t *list, uint32_t n, const TopArgs &a, int r, V
 // counts' too: an exponential a value, not a logit.
 //
 // 1024 rows of 151936, four after the other on a CU: 130 us, 33 a row: 14 for
-// the loads and counts, which all CUs together read at 5.7 TB/s, then 4 for
+// the loads and counts (279 MB in all: 5 TB/s meanwhile), then 4 for
 // the blocks' totals, 1 for the k-th's place, 4 to list and 1 to order the 64,
 // and the waves' differences; the memory is idle in the second half (see
 // k_filter_counts).  4 rows of 128256, where only a row's time counts: 20 us.
