@@ -578,8 +578,10 @@ def _row_call(fn, device, stream, *args):
     """fn(*args, stream) on device number `device`."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    raw = getattr(stream, "cuda_stream", stream) or None
+        # the handle alone (without the Stream object around it: 1 us of a call's 10)
+        raw = torch._C._cuda_getCurrentRawStream(device) or None
+    else:
+        raw = getattr(stream, "cuda_stream", stream) or None
     if device == torch.cuda.current_device():
         rc = fn(*args, raw)
     else:
@@ -655,28 +657,30 @@ def _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
     if teacher_ids.dim() != 2:
         raise ValueError("teacher_ids must be [rows, k]")
     k, dev = teacher_ids.shape[1], logits.get_device()
-    return dev, B, V, (logits.data_ptr(), dt, B, V, stride, m, words,
+    return dev, B, (logits.data_ptr(), dt, B, V, stride, m, words,
                        _row_arg(teacher_ids, torch.int32, "teacher_ids", dev, B, k),
                        _row_arg(teacher_logits, torch.float32, "teacher_logits", dev, B, k), k, temperature)
 
 
-def _grad_arg(grad, logits, B, V):
+def _grad_arg(grad, logits, args):
     """(address, row stride) of a gradient: the logits themselves, or rows apart from them."""
+    b, dt, B, V, x_stride = args[:5]
     if grad.dtype is not logits.dtype or grad.get_device() != logits.get_device():
         raise ValueError("out_grad must have the logits' dtype and device")
-    if grad.dim() != 2 or grad.stride(1) != 1 or grad.shape[0] < B or grad.shape[1] < V:
+    shape, strides = grad.shape, grad.stride()
+    if len(shape) != 2 or strides[1] != 1 or shape[0] < B or shape[1] < V:
         raise ValueError("out_grad must be [rows, >= vocab] with unit column stride")
-    stride = max(grad.stride(0), V) if B == 1 else grad.stride(0)
+    a, stride = grad.data_ptr(), strides[0]
     if stride < V:
-        raise ValueError("out_grad's rows overlap")
-    a, b = grad.data_ptr(), logits.data_ptr()
-    if a != b or stride != (max(logits.stride(0), V) if B == 1 else logits.stride(0)):
-        size = logits.element_size()
-        at = (a - b) // size % stride  # rows that lie between the logits' rows
-        if logits.stride(0) == stride and V <= at <= stride - V:
-            return a, stride
-        if B and a < b + ((B - 1) * logits.stride(0) + V) * size and b < a + ((B - 1) * stride + V) * size:
-            raise ValueError("out_grad overlaps the logits (it may only be the same rows)")
+        if B > 1:
+            raise ValueError("out_grad's rows overlap")
+        stride = V
+    if a != b or stride != x_stride:
+        size = 2 if dt == DTYPE_BF16 else 4
+        if B and a < b + ((B - 1) * x_stride + V) * size and b < a + ((B - 1) * stride + V) * size:
+            # they may still lie between the logits' rows
+            if x_stride != stride or not V <= (a - b) // size % stride <= stride - V:
+                raise ValueError("out_grad overlaps the logits (it may only be the same rows)")
     return a, stride
 
 
@@ -690,11 +694,11 @@ def distill_topk(logits, mask, teacher_ids, teacher_logits, temperature, out_los
     in out_grad [rows, >= vocab] of the logits' dtype (it may be `logits`)."""
     import torch
     L = _row_lib()
-    dev, B, V, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
+    dev, B, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
     f32 = torch.float32
     if (weight is None) != (out_grad is None):
         raise ValueError("weight and out_grad go together")
-    g, gs = (None, 0) if out_grad is None else _grad_arg(out_grad, logits, B, V)
+    g, gs = (None, 0) if out_grad is None else _grad_arg(out_grad, logits, args)
     _row_call(L.cg_distill_topk, dev, stream, *args, _row_arg(out_loss, f32, "out_loss", dev, B),
               None if out_lse is None else _row_arg(out_lse, f32, "out_lse", dev, B),
               None if weight is None else _row_arg(weight, f32, "weight", dev, B), g, gs)
@@ -705,8 +709,8 @@ def distill_topk_grad(logits, mask, teacher_ids, teacher_logits, temperature, ls
     """cg_distill_topk_grad: distill_topk's gradient alone, from the lse it wrote."""
     import torch
     L = _row_lib()
-    dev, B, V, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
-    g, gs = _grad_arg(out_grad, logits, B, V)
+    dev, B, args = _distill_args(logits, mask, teacher_ids, teacher_logits, temperature, vocab)
+    g, gs = _grad_arg(out_grad, logits, args)
     _row_call(L.cg_distill_topk_grad, dev, stream, *args, _row_arg(lse, torch.float32, "lse", dev, B),
               _row_arg(weight, torch.float32, "weight", dev, B), g, gs)
 
