@@ -648,15 +648,16 @@ struct FineDraw {
     }
 };
 
-// Launches KERNEL<NP, SPANS> with as many pieces as rows of V ids need (3: the
-// largest skew); longer rows keep nothing between passes and are read in
-// spans of 8.
+// Launches KERNEL<8, SPANS>: rows of up to 8 pieces (3: the largest skew) stay
+// in registers (64 rows of 32000 without filters 36.6 us, in spans 41.6),
+// longer ones keep nothing between passes and are read in spans of 8.  16 pieces, 64 of a thread's 128 registers, left the searches too few:
+// top 50 of 600 rows of 60000 took 126 us so, 99 in spans, top 20 of 256 rows
+// of 50021 33 and 28 us; spans of 16 three times as long as of 8.
 #define CG_LAUNCH_FINE(KERNEL, V, BATCH, STREAM, ARGS)                                              \
     do {                                                                                            \
-        const int pieces_ = ((V) + 3 + kFinePieceIds - 1) / kFinePieceIds;                          \
         const dim3 grid_(BATCH), block_(kRowThreads);                                               \
-        if (pieces_ <= 8) hipLaunchKernelGGL((KERNEL<8, false>), grid_, block_, 0, STREAM, ARGS);   \
-        else if (pieces_ <= 16) hipLaunchKernelGGL((KERNEL<16, false>), grid_, block_, 0, STREAM, ARGS); \
+        if ((V) + 3 <= 8 * kFinePieceIds)                                                           \
+            hipLaunchKernelGGL((KERNEL<8, false>), grid_, block_, 0, STREAM, ARGS);                 \
         else hipLaunchKernelGGL((KERNEL<8, true>), grid_, block_, 0, STREAM, ARGS);                 \
     } while (0)
 
