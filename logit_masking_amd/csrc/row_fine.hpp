@@ -650,9 +650,10 @@ struct FineDraw {
 
 // Launches KERNEL<8, SPANS>: rows of up to 8 pieces (3: the largest skew) stay
 // in registers (64 rows of 32000 without filters 36.6 us, in spans 41.6),
-// longer ones keep nothing between passes and are read in spans of 8.  16 pieces, 64 of a thread's 128 registers, left the searches too few:
-// top 50 of 600 rows of 60000 took 126 us so, 99 in spans, top 20 of 256 rows
-// of 50021 33 and 28 us; spans of 16 three times as long as of 8.
+// longer ones keep nothing between passes and are read in spans of 8.  16
+// pieces, 64 of a thread's 128 registers, left the searches too few: top 50 of
+// 600 rows of 60000 took 126 us so, 99 in spans, top 20 of 256 rows of 50021
+// 33 and 28 us; spans of 16 took up to three times as long as spans of 8.
 #define CG_LAUNCH_FINE(KERNEL, V, BATCH, STREAM, ARGS)                                              \
     do {                                                                                            \
         const dim3 grid_(BATCH), block_(kRowThreads);                                               \

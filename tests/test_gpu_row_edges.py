@@ -145,6 +145,35 @@ def test_rows_do_not_know_each_other(V, B, dtype):
                     [None if g is None else g[:3] for g in part], dtype, way == "grad")
 
 
+@pytest.mark.parametrize("dtype,V", [(d, v + n) for d, limits in (("float32", (16381, 32765, 65533)),
+                                                                  ("bfloat16", (32761, 65529, 131065, 163833)))
+                                     for v in limits for n in (0, 1)])
+def test_at_the_variants_limits(dtype, V):
+    """Rows as long as a variant takes them, and one id longer, starting as far off 16 bytes as they can and on them."""
+    import torch
+    say("limits", dtype, V)
+    rng = np.random.default_rng(V)
+    B = 3
+    for off, pad in ((3 if dtype == "float32" else 7, 0), (0, -V % 8), (1, 2)):
+        flat = torch.full((B * (V + pad) + off + 64,), INF, dtype=getattr(torch, dtype), device="cuda")
+        x = flat[off:off + B * (V + pad)].view(B, V + pad)
+        x[:, :V] = F.make(rng, B, V, dtype)
+        x[:, V - 1] = 9.5  # the last id is one that counts
+        allowed = F.masks(rng, B, V)
+        allowed[0, V - 1] = True
+        s = F.settings(rng, B, "p")
+        draw(x, allowed, s, vocab=V)
+        top(x, allowed, 6, vocab=V)
+        draw(x, None, s, vocab=V)
+        top(x, None, 6, vocab=V)
+        ids, t = D.teacher(rng, x, None, 8, V)
+        ids[0, 4] = V - 1
+        w = np.array([0.5, 1.0, 2.0], dtype=np.float32)
+        xs = x[:, :V].double().cpu().numpy()
+        for way in ("both", "grad"):
+            D.check(xs, allowed, ids, t, 1.0, w, D.run(x, F.pack(allowed), ids, t, 1.0, way, w, vocab=V), dtype, way == "grad")
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_longest_vocabulary(dtype):
     import torch
